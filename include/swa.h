@@ -309,6 +309,111 @@ swa_status_t swa_decode_rope(const void *q, const void *k_cache, const void *v_c
                              swa_stream_t stream);
 
 /*
+ * The rolling buffer held in 8 bits: half the memory and half the decode
+ * traffic of the 16-bit one.  The pages have no counterpart; they bound decode
+ * by the cache's bytes and count its memory per entry (section 3.4 and 3.3 of
+ * the manon006 review), which is what this halves.
+ *   k_cache, v_cache : [B, W, Hkv, D] codes, one byte each, e4m3 floating point
+ *                      (4 exponent, 3 mantissa bits, largest 448)
+ *   k_scale, v_scale : float32 [B, ceil(W / block), Hkv]; the element is
+ *                      code * scale of its block of slots, block = slot / `block`
+ *   block            : 16, 32, 64 or 128 slots
+ * A scale is the smallest power of two with which the block's largest finite
+ * magnitude is at most 448 (exponent held to [-117, 119]); 0 for a block of
+ * zeros.  Elements are rounded to nearest, ties to even; NaN and infinities are
+ * stored as NaN.  Slot rule, positions, windows and errors are those of the
+ * 16-bit calls.  A buffer needs no set-up: slots that no position has reached
+ * are neither read nor written.
+ */
+
+/* swa_cache_append_q8 -- swa_cache_append into the 8-bit buffer.  Every block
+ * that receives a token is quantised anew from what it then holds: the new
+ * tokens, and the values that its other written slots stand for.  (A scale
+ * that moves rounds only elements below 2^-6 of it.)  A 16-bit rolling buffer
+ * is converted by one call with pos = 0, T = W (slot s then holds slot s). */
+swa_status_t swa_cache_append_q8(const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+                                 float *k_scale, float *v_scale, const int32_t *pos, int B, int T,
+                                 int Hkv, int D, int W, int block, swa_stream_t stream);
+
+/* swa_decode_q8 -- swa_decode over the 8-bit buffer.  The workspace is that of
+ * swa_decode: swa_decode_workspace_size(B, Hq, Hkv, D, W). */
+swa_status_t swa_decode_q8(const void *q, const void *k_cache, const void *v_cache,
+                           const float *k_scale, const float *v_scale, const int32_t *pos, void *out,
+                           int B, int Hq, int Hkv, int D, int W, int block, float scale,
+                           void *workspace, size_t workspace_bytes, swa_stream_t stream);
+
+/* swa_prefill_chunk_q8 -- swa_prefill_chunk through the 8-bit buffer: query
+ * s0+t attends to the cached positions in its window, as the codes stand for
+ * them, and causally to the chunk's own 16-bit keys and values; then the chunk
+ * is appended as by swa_cache_append_q8.  Requires C <= W.  workspace: at least
+ * swa_prefill_chunk_q8_workspace_size() bytes, 256-byte aligned; it holds the
+ * window widened to bf16 (exactly) during the call. */
+swa_status_t swa_prefill_chunk_q8(const void *q, const void *k, const void *v, void *k_cache,
+                                  void *v_cache, float *k_scale, float *v_scale,
+                                  const int32_t *start_pos, void *out, int B, int C, int Hq, int Hkv,
+                                  int D, int W, int block, float scale, void *workspace,
+                                  size_t workspace_bytes, swa_stream_t stream);
+size_t swa_prefill_chunk_q8_workspace_size(int B, int Hkv, int D, int W);
+
+/*
+ * The fixed-size cache with eviction by accumulated attention weight: like the
+ * rolling buffer its memory does not grow with the sequence, but what leaves is
+ * the key that has received the least attention, not the oldest.  The pages
+ * have no counterpart; they keep a recent window, or a window and the first
+ * tokens (attention sinks), both of which this keeps as well.
+ *   k_cache, v_cache : [B, M, Hkv, D] bf16; each KV head fills its M slots on
+ *                      its own
+ *   slot_pos         : int32 [B, Hkv, M], the position each slot holds; < 0: free
+ *   weights          : float32 [B, Hkv, M], the softmax weight each slot has
+ *                      received, summed over the queries so far and over the
+ *                      query heads of the group
+ * A prompt: swa_prefill (W >= N), swa_prefill_weights, swa_cache_keep.  A token:
+ * swa_cache_evict_append, then swa_decode_weights.  Positions p < S (sinks) and
+ * the last R positions, the new token included, are never evicted: S >= 0,
+ * R >= 1, S + R <= M.
+ */
+
+/* swa_cache_evict_append -- store the token at position pos[b], k_new, v_new
+ * [B, Hkv, D], in one slot of each KV head: the slot that already holds pos[b],
+ * else the lowest free one, else the one of least weight among those whose
+ * position q has S <= q <= pos[b] - R (ties: the lowest slot; NaN counts as
+ * infinity).  Its slot_pos becomes pos[b], its weight 0.  slots: int32 [B, Hkv],
+ * receives the slot taken, or NULL.  If no slot may be evicted nothing is
+ * written, slots gets -1 and SWA_ERR_INVALID_ARG is recorded (as for pos[b] <
+ * 0); it cannot happen to a cache that only these calls have filled. */
+swa_status_t swa_cache_evict_append(const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+                                    int32_t *slot_pos, float *weights, const int32_t *pos,
+                                    int32_t *slots, int B, int Hkv, int D, int M, int S, int R,
+                                    swa_stream_t stream);
+
+/* swa_decode_weights -- swa_decode over the slots 0 .. min(pos[b]+1, M)-1 that
+ * are not free (what a free slot holds is never used), and
+ *   weights_out[b,g,s] = weights[b,g,s] + sum over the group's heads of the
+ *                        softmax weight of slot s.
+ * weights NULL: from 0; weights_out may be weights.  A KV head that holds no
+ * token gives an output of 0.  A sequence with pos[b] < 0 is skipped.
+ * workspace: at least swa_decode_weights_workspace_size() bytes, 256-byte
+ * aligned, as for swa_decode.  At most 2048 query heads to a KV head. */
+swa_status_t swa_decode_weights(const void *q, const void *k_cache, const void *v_cache,
+                                const int32_t *slot_pos, const float *weights, float *weights_out,
+                                const int32_t *pos, void *out, int B, int Hq, int Hkv, int D, int M,
+                                float scale, void *workspace, size_t workspace_bytes,
+                                swa_stream_t stream);
+size_t swa_decode_weights_workspace_size(int B, int Hq, int Hkv, int D, int M);
+
+/* swa_cache_keep -- cut prompts of lens[b] positions (int32 [B], 0 .. N), k, v
+ * [B, N, Hkv, D] with weights float32 [B, Hkv, N], to the M slots of a cache:
+ * every position if lens[b] <= M; else the first S, the last R and, of the
+ * others, the M - S - R of largest weight (ties: the lowest position; NaN
+ * counts as infinity), in the order of their positions.  weights_out [B, Hkv,
+ * M] receives the kept weights.  Unused slots get slot_pos -1 and weight 0;
+ * their K and V are left as they were.  A length outside [0, N] is recorded as
+ * SWA_ERR_INVALID_ARG and keeps nothing. */
+swa_status_t swa_cache_keep(const void *k, const void *v, const float *weights, const int32_t *lens,
+                            void *k_cache, void *v_cache, int32_t *slot_pos, float *weights_out, int B,
+                            int N, int Hkv, int D, int M, int S, int R, swa_stream_t stream);
+
+/*
  * swa_get_device_status -- synchronise `stream`, then return (and reset to
  * SWA_OK) the device status word that kernels of this library set when a
  * bounded wait runs out.  Returns SWA_ERR_CUDA if synchronisation fails.

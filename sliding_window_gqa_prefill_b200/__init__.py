@@ -23,7 +23,9 @@ __all__ = [
     "swa_decode_sinks", "swa_rope", "swa_get_device_status", "swa_set_wait_limit_ns",
     "swa_selftest_wait_timeout", "swa_selftest_exp2", "SWA_OK", "SWA_ERR_INVALID_ARG",
     "SWA_ERR_UNSUPPORTED", "SWA_ERR_CUDA", "SWA_ERR_TIMEOUT", "SWA_WINDOW_EXCL_LEFT",
-    "SWA_WINDOW_INCL_LEFT", "bounds_checked",
+    "SWA_WINDOW_INCL_LEFT", "bounds_checked", "swa_cache_append_q8", "swa_decode_q8", "swa_prefill_chunk_q8",
+    "swa_prefill_chunk_q8_workspace_size", "swa_cache_evict_append", "swa_decode_weights",
+    "swa_decode_weights_workspace_size", "swa_cache_keep",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -34,7 +36,8 @@ LIB_PATH = os.path.join(_PKG, "libswa.so")
 DEBUG_LIB_PATH = os.path.join(_PKG, "libswa_debug.so")
 HEADER = os.path.join(_ROOT, "include", "swa.h")
 _SOURCES = [os.path.join(_PKG, "csrc", f) for f in
-            ("swa_api.cu", "device_common.cuh", "prefill_plan.cuh", "prefill_kernel.cuh", "decode_kernel.cuh")]
+            ("swa_api.cu", "device_common.cuh", "prefill_plan.cuh", "prefill_kernel.cuh", "decode_kernel.cuh",
+             "q8_kernel.cuh", "evict_kernel.cuh")]
 
 SWA_OK, SWA_ERR_INVALID_ARG, SWA_ERR_UNSUPPORTED, SWA_ERR_CUDA, SWA_ERR_TIMEOUT = 0, 1, 2, 3, 4
 SWA_WINDOW_EXCL_LEFT, SWA_WINDOW_INCL_LEFT = 0, 1
@@ -127,6 +130,20 @@ def lib() -> ctypes.CDLL:
             for fn in (L.swa_prefill_sinks, L.swa_cache_append_sinks, L.swa_decode_sinks,
                        L.swa_prefill_chunk_sinks):
                 fn.restype = ctypes.c_int
+            z = ctypes.c_size_t
+            L.swa_cache_append_q8.argtypes = [vp] * 7 + [i] * 6 + [st]
+            L.swa_decode_q8.argtypes = [vp] * 7 + [i] * 6 + [f, vp, z, st]
+            L.swa_prefill_chunk_q8.argtypes = [vp] * 9 + [i] * 7 + [f, vp, z, st]
+            L.swa_cache_evict_append.argtypes = [vp] * 8 + [i] * 6 + [st]
+            L.swa_decode_weights.argtypes = [vp] * 8 + [i] * 5 + [f, vp, z, st]
+            L.swa_cache_keep.argtypes = [vp] * 8 + [i] * 7 + [st]
+            for fn in (L.swa_cache_append_q8, L.swa_decode_q8, L.swa_prefill_chunk_q8, L.swa_cache_evict_append,
+                       L.swa_decode_weights, L.swa_cache_keep):
+                fn.restype = ctypes.c_int
+            L.swa_prefill_chunk_q8_workspace_size.argtypes = [i] * 4
+            L.swa_decode_weights_workspace_size.argtypes = [i] * 5
+            for fn in (L.swa_prefill_chunk_q8_workspace_size, L.swa_decode_weights_workspace_size):
+                fn.restype = ctypes.c_size_t
             L.swa_decode_workspace_size.argtypes = [i, i, i, i, i]
             L.swa_decode_workspace_size.restype = ctypes.c_size_t
             L.swa_get_device_status.argtypes = [st]
@@ -408,3 +425,207 @@ def swa_decode_sinks(q, k_cache, v_cache, k_sink, v_sink, pos, scale: float, out
         _bf16(out, "out", (B, Hq, D)), B, Hq, Hkv, D, W, S, float(scale), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _stream_handle(stream)), "swa_decode_sinks")
     return out
+
+
+# ------------------------------------------------------------------ 8-bit rolling buffer
+
+def _ptr(t, name: str, dtype, shape, device: int) -> int:
+    """The address of a contiguous CUDA tensor of this type and shape on the
+    current device, on which the library launches."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name}: expected a CUDA tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on cuda:{t.get_device()}, but the current device is cuda:{device}")
+    return t.data_ptr()
+
+
+def _dims(t, name: str, n: int):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dim() != n:
+        raise ValueError(f"{name}: expected a tensor of {n} dimensions")
+    return t.shape
+
+
+def _empty(shape, dtype, stream):
+    """A new tensor on the current device, from the memory of the stream that
+    will write it (so its reuse is ordered after that work)."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device="cuda")
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device="cuda")
+
+
+def _scratch(workspace, need: int, device: int, stream):
+    """(tensor, address, bytes) of the caller's workspace, or of a new one of `need` bytes."""
+    import torch
+    if workspace is None:
+        workspace = _empty(max(need, 256), torch.uint8, stream)
+    elif not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
+        raise TypeError("workspace: expected a contiguous CUDA tensor")
+    elif workspace.get_device() != device:
+        raise ValueError(f"workspace: not on the current device cuda:{device}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _q8_cache(k_cache, v_cache, k_scale, v_scale, block: int, device: int):
+    """Addresses and sizes of an 8-bit buffer: ((k, v, k scales, v scales), (B, W, Hkv, D))."""
+    import torch
+    dims = _dims(k_cache, "k_cache", 4)
+    B, W, Hkv, D = dims
+    if block not in (16, 32, 64, 128):
+        raise ValueError(f"block: expected 16, 32, 64 or 128, got {block}")
+    scales = (B, (W + block - 1) // block, Hkv)
+    return (_ptr(k_cache, "k_cache", torch.float8_e4m3fn, dims, device),
+            _ptr(v_cache, "v_cache", torch.float8_e4m3fn, dims, device),
+            _ptr(k_scale, "k_scale", torch.float32, scales, device),
+            _ptr(v_scale, "v_scale", torch.float32, scales, device)), dims
+
+
+def swa_cache_append_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, pos, block: int = 64, stream=None) -> None:
+    """Write k_new/v_new [B,T,Hkv,D] bf16 at slots (pos[b]+t) mod W of the 8-bit
+    buffers [B,W,Hkv,D] float8_e4m3fn, whose values are code * scale, scales
+    float32 [B,ceil(W/block),Hkv] per block of slots and head."""
+    import torch
+    dev = torch.cuda.current_device()
+    cache, (B, W, Hkv, D) = _q8_cache(k_cache, v_cache, k_scale, v_scale, block, dev)
+    T = _dims(k_new, "k_new", 4)[1]
+    new = (B, T, Hkv, D)
+    _check(lib().swa_cache_append_q8(
+        _ptr(k_new, "k_new", torch.bfloat16, new, dev), _ptr(v_new, "v_new", torch.bfloat16, new, dev), *cache,
+        _ptr(pos, "pos", torch.int32, (B,), dev), B, T, Hkv, D, W, block, _stream_handle(stream)),
+        "swa_cache_append_q8")
+
+
+def swa_decode_q8(q, k_cache, v_cache, k_scale, v_scale, pos, scale: float, block: int = 64, out=None, workspace=None,
+                  stream=None):
+    """swa_decode over an 8-bit buffer (swa_cache_append_q8).  q [B,Hq,D] bf16;
+    workspace as for swa_decode."""
+    import torch
+    dev = torch.cuda.current_device()
+    cache, (B, W, Hkv, D) = _q8_cache(k_cache, v_cache, k_scale, v_scale, block, dev)
+    rows = _dims(q, "q", 3)
+    Hq = rows[1]
+    args = (_ptr(q, "q", torch.bfloat16, (B, Hq, D), dev), *cache, _ptr(pos, "pos", torch.int32, (B,), dev))
+    if out is None:
+        out = _empty(rows, torch.bfloat16, stream)
+    L = lib()
+    workspace, ws, size = _scratch(workspace, L.swa_decode_workspace_size(B, Hq, Hkv, D, W), dev, stream)
+    _check(L.swa_decode_q8(*args, _ptr(out, "out", torch.bfloat16, rows, dev), B, Hq, Hkv, D, W, block, scale, ws, size,
+                           _stream_handle(stream)), "swa_decode_q8")
+    return out
+
+
+def swa_prefill_chunk_q8_workspace_size(B: int, Hkv: int, D: int, W: int) -> int:
+    return int(lib().swa_prefill_chunk_q8_workspace_size(B, Hkv, D, W))
+
+
+def swa_prefill_chunk_q8(q, k, v, k_cache, v_cache, k_scale, v_scale, start_pos, W: int, scale: float, block: int = 64,
+                         out=None, workspace=None, stream=None):
+    """swa_prefill_chunk through an 8-bit buffer: the chunk attends to the cached
+    window and to its own 16-bit keys, then is appended (updates the buffers)."""
+    import torch
+    dev = torch.cuda.current_device()
+    cache, (B, slots, Hkv, D) = _q8_cache(k_cache, v_cache, k_scale, v_scale, block, dev)
+    if slots != W:
+        raise ValueError(f"k_cache: expected {W} slots, got {slots}")
+    rows = _dims(q, "q", 4)
+    C, Hq = rows[1], rows[2]
+    new = (B, C, Hkv, D)
+    args = (_ptr(q, "q", torch.bfloat16, (B, C, Hq, D), dev), _ptr(k, "k", torch.bfloat16, new, dev),
+            _ptr(v, "v", torch.bfloat16, new, dev), *cache, _ptr(start_pos, "start_pos", torch.int32, (B,), dev))
+    if out is None:
+        out = _empty(rows, torch.bfloat16, stream)
+    L = lib()
+    workspace, ws, size = _scratch(workspace, L.swa_prefill_chunk_q8_workspace_size(B, Hkv, D, W), dev, stream)
+    _check(L.swa_prefill_chunk_q8(*args, _ptr(out, "out", torch.bfloat16, rows, dev), B, C, Hq, Hkv, D, W, block, scale,
+                                  ws, size, _stream_handle(stream)), "swa_prefill_chunk_q8")
+    return out
+
+
+# ------------------------------------------------------------------ fixed-size cache with eviction
+
+def swa_cache_evict_append(k_new, v_new, k_cache, v_cache, slot_pos, weights, pos, S: int, R: int, slots=None,
+                           stream=None):
+    """Store the token at pos[b], k_new/v_new [B,Hkv,D] bf16, in one slot of each
+    KV head of the caches [B,M,Hkv,D]: the one that holds pos[b], else the lowest
+    free one (slot_pos < 0), else the one of least weight that is neither of the
+    first S positions nor of the last R.  Updates slot_pos int32 and weights
+    float32 [B,Hkv,M]; returns the slots taken, int32 [B,Hkv] (-1: none)."""
+    import torch
+    dev = torch.cuda.current_device()
+    dims = _dims(k_cache, "k_cache", 4)
+    B, M, Hkv, D = dims
+    new, state = (B, Hkv, D), (B, Hkv, M)
+    bf16 = torch.bfloat16
+    args = (_ptr(k_new, "k_new", bf16, new, dev), _ptr(v_new, "v_new", bf16, new, dev),
+            _ptr(k_cache, "k_cache", bf16, dims, dev), _ptr(v_cache, "v_cache", bf16, dims, dev),
+            _ptr(slot_pos, "slot_pos", torch.int32, state, dev), _ptr(weights, "weights", torch.float32, state, dev),
+            _ptr(pos, "pos", torch.int32, (B,), dev))
+    if slots is None:
+        slots = _empty((B, Hkv), torch.int32, stream)
+    _check(lib().swa_cache_evict_append(*args, _ptr(slots, "slots", torch.int32, (B, Hkv), dev), B, Hkv, D, M, S, R,
+                                        _stream_handle(stream)), "swa_cache_evict_append")
+    return slots
+
+
+def swa_decode_weights_workspace_size(B: int, Hq: int, Hkv: int, D: int, M: int) -> int:
+    return int(lib().swa_decode_weights_workspace_size(B, Hq, Hkv, D, M))
+
+
+def swa_decode_weights(q, k_cache, v_cache, slot_pos, weights, pos, scale: float, weights_out=None, out=None,
+                       workspace=None, stream=None):
+    """Decode one token per sequence over the slots of a fixed-size cache
+    [B,M,Hkv,D] that hold a position (slot_pos [B,Hkv,M] int32 >= 0), and add the
+    softmax weight each slot receives to `weights` [B,Hkv,M] float32 (None: from
+    0).  weights_out: where the sums go (default: weights itself, in place).
+    Returns (out [B,Hq,D], weights_out)."""
+    import torch
+    dev = torch.cuda.current_device()
+    dims = _dims(k_cache, "k_cache", 4)
+    B, M, Hkv, D = dims
+    rows = _dims(q, "q", 3)
+    Hq = rows[1]
+    state = (B, Hkv, M)
+    bf16, f32 = torch.bfloat16, torch.float32
+    args = (_ptr(q, "q", bf16, (B, Hq, D), dev), _ptr(k_cache, "k_cache", bf16, dims, dev),
+            _ptr(v_cache, "v_cache", bf16, dims, dev), _ptr(slot_pos, "slot_pos", torch.int32, state, dev),
+            None if weights is None else _ptr(weights, "weights", f32, state, dev))
+    if weights_out is None:
+        weights_out = _empty(state, f32, stream) if weights is None else weights
+    if out is None:
+        out = _empty(rows, bf16, stream)
+    L = lib()
+    workspace, ws, size = _scratch(workspace, L.swa_decode_weights_workspace_size(B, Hq, Hkv, D, M), dev, stream)
+    _check(L.swa_decode_weights(*args, _ptr(weights_out, "weights_out", f32, state, dev),
+                                _ptr(pos, "pos", torch.int32, (B,), dev), _ptr(out, "out", bf16, rows, dev), B, Hq, Hkv,
+                                D, M, scale, ws, size, _stream_handle(stream)), "swa_decode_weights")
+    return out, weights_out
+
+
+def swa_cache_keep(k, v, weights, lens, k_cache, v_cache, slot_pos, weights_out, S: int, R: int, stream=None) -> None:
+    """Cut prompts of lens[b] positions (int32 [B]), k/v [B,N,Hkv,D] bf16 with
+    accumulated weights [B,Hkv,N] float32, to the M slots of the caches
+    [B,M,Hkv,D]: the first S positions, the last R and those of the largest
+    weight between.  Writes the caches, slot_pos int32 and weights_out float32
+    [B,Hkv,M]."""
+    import torch
+    dev = torch.cuda.current_device()
+    prompt = _dims(k, "k", 4)
+    B, N, Hkv, D = prompt
+    M = _dims(k_cache, "k_cache", 4)[1]
+    dims, state = (B, M, Hkv, D), (B, Hkv, M)
+    bf16, f32 = torch.bfloat16, torch.float32
+    _check(lib().swa_cache_keep(
+        _ptr(k, "k", bf16, prompt, dev), _ptr(v, "v", bf16, prompt, dev),
+        _ptr(weights, "weights", f32, (B, Hkv, N), dev), _ptr(lens, "lens", torch.int32, (B,), dev),
+        _ptr(k_cache, "k_cache", bf16, dims, dev), _ptr(v_cache, "v_cache", bf16, dims, dev),
+        _ptr(slot_pos, "slot_pos", torch.int32, state, dev), _ptr(weights_out, "weights_out", f32, state, dev),
+        B, N, Hkv, D, M, S, R, _stream_handle(stream)), "swa_cache_keep")

@@ -122,6 +122,82 @@ __device__ __forceinline__ uint32_t swz_off(int r, int ch, int row_bytes) {
     return (uint32_t)(r * row_bytes + ((ch ^ (r & 7)) << 4));
 }
 
+// The tail of a decode block whose warps have left their partial results
+// {o[D], m, l} per head in mg [warp][G][D+2]: merges them and, with CLUSTER,
+// the blocks of the cluster too (each merges and writes a quarter of the
+// outputs); else writes the output if the window is one split, and the split's
+// partial result to the workspace if it is not.  out_rows: rows of out.
+template <int D, int G, bool CLUSTER>
+__device__ __forceinline__ void decode_merge(float *mg, int b, int qrow, long long out_rows, int g, int Hkv, int split,
+                                             int nsplit, int nsplit_max, __nv_bfloat16 *out, float2 *ws_ml,
+                                             float *ws_o) {
+    const int Hq = Hkv * G;
+    __syncthreads();
+    float *part = mg + kDecodeWarps * G * (D + 2);  // [G][D+2]: the block's merge (cluster modes)
+    for (int idx = threadIdx.x; idx < G * D; idx += blockDim.x) {
+        const int h = idx / D, d = idx % D;
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kDecodeWarps; ++w) m = fmaxf(m, mg[(w * G + h) * (D + 2) + D]);
+        float l = 0.f, acc = 0.f;
+#pragma unroll
+        for (int w = 0; w < kDecodeWarps; ++w) {
+            const float *src = mg + (w * G + h) * (D + 2);
+            const float sc = (src[D] == -INFINITY) ? 0.f : ex2_approx(src[D] - m);
+            l += src[D + 1] * sc;
+            acc += src[d] * sc;
+        }
+        if (CLUSTER) {
+            part[h * (D + 2) + d] = acc;
+            if (d == 0) {
+                part[h * (D + 2) + D] = m;
+                part[h * (D + 2) + D + 1] = l;
+            }
+        } else if (nsplit == 1) {
+            const size_t oi = ((size_t)qrow * Hq + g * G + h) * D + d;
+            if (in_bounds((long long)oi, out_rows * Hq * D)) out[oi] = __float2bfloat16_rn(acc / l);
+        } else {
+            const size_t slot = ((size_t)(b * Hkv + g) * nsplit_max + split) * G + h;
+            if (!in_bounds(split, nsplit_max)) continue;
+            ws_o[slot * D + d] = acc;
+            if (d == 0) ws_ml[slot] = make_float2(m, l);
+        }
+    }
+    if constexpr (CLUSTER) {
+        // every block of the cluster reaches both barriers: the only returns
+        // above depend on (b) alone, which the cluster shares
+        cluster_sync_all();
+        {   // each block of the cluster merges and writes a quarter of the outputs
+            static_assert((G * D) % kDecodeClusterSplits == 0, "outputs per block");
+            constexpr int kPer = G * D / kDecodeClusterSplits;
+            const int i0 = (int)cluster_rank() * kPer;
+            for (int idx = i0 + threadIdx.x; idx < i0 + kPer; idx += blockDim.x) {
+                const int h = idx / D, d = idx % D;
+                const uint32_t row = smem_addr(part + h * (D + 2));
+                float mr[kDecodeClusterSplits], lr[kDecodeClusterSplits], ar[kDecodeClusterSplits];
+                float m = -INFINITY;
+#pragma unroll
+                for (int r = 0; r < kDecodeClusterSplits; ++r) {
+                    mr[r] = ld_peer_f32(row + D * 4, r);
+                    lr[r] = ld_peer_f32(row + (D + 1) * 4, r);
+                    ar[r] = ld_peer_f32(row + d * 4, r);
+                    m = fmaxf(m, mr[r]);
+                }
+                float l = 0.f, acc = 0.f;
+#pragma unroll
+                for (int r = 0; r < kDecodeClusterSplits; ++r) {
+                    const float sc = (mr[r] == -INFINITY) ? 0.f : ex2_approx(mr[r] - m);
+                    l += lr[r] * sc;
+                    acc += ar[r] * sc;
+                }
+                const size_t oi = ((size_t)qrow * Hq + g * G + h) * D + d;
+                if (in_bounds((long long)oi, out_rows * Hq * D)) out[oi] = __float2bfloat16_rn(acc / l);
+            }
+        }
+        cluster_sync_all();                          // peers' shared memory stays until read
+    }
+}
+
 // Partial result of one (sequence, kv head, split): per head m (base-2 max),
 // l (sum of 2^(s-m)) and o[D] (sum of 2^(s-m) v).  Layout in the workspace:
 // ml[((b*Hkv + g)*nsplit_max + s)*G + h] = {m, l};  o[...*D + d].
@@ -371,70 +447,8 @@ swa_decode_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__re
             dst[D + 1] = l_run;
         }
     }
-    __syncthreads();
-    float *part = mg + kDecodeWarps * G * (D + 2);  // [G][D+2]: the block's merge (cluster modes)
-    for (int idx = threadIdx.x; idx < G * D; idx += blockDim.x) {
-        const int h = idx / D, d = idx % D;
-        float m = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kDecodeWarps; ++w) m = fmaxf(m, mg[(w * G + h) * (D + 2) + D]);
-        float l = 0.f, acc = 0.f;
-#pragma unroll
-        for (int w = 0; w < kDecodeWarps; ++w) {
-            const float *src = mg + (w * G + h) * (D + 2);
-            const float sc = (src[D] == -INFINITY) ? 0.f : ex2_approx(src[D] - m);
-            l += src[D + 1] * sc;
-            acc += src[d] * sc;
-        }
-        if (CLUSTER) {
-            part[h * (D + 2) + d] = acc;
-            if (d == 0) {
-                part[h * (D + 2) + D] = m;
-                part[h * (D + 2) + D + 1] = l;
-            }
-        } else if (nsplit == 1) {
-            const size_t oi = ((size_t)qrow * Hq + g * G + h) * D + d;
-            if (in_bounds((long long)oi, (long long)gridDim.z * Hq * D)) out[oi] = __float2bfloat16_rn(acc / l);
-        } else {
-            const size_t slot = ((size_t)(b * Hkv + g) * nsplit_max + split) * G + h;
-            if (!in_bounds(split, nsplit_max)) continue;
-            ws_o[slot * D + d] = acc;
-            if (d == 0) ws_ml[slot] = make_float2(m, l);
-        }
-    }
-    if constexpr (CLUSTER) {
-        // every block of the cluster reaches both barriers: the only returns
-        // above depend on (b) alone, which the cluster shares
-        cluster_sync_all();
-        {   // each block of the cluster merges and writes a quarter of the outputs
-            static_assert((G * D) % kDecodeClusterSplits == 0, "outputs per block");
-            constexpr int kPer = G * D / kDecodeClusterSplits;
-            const int i0 = (int)cluster_rank() * kPer;
-            for (int idx = i0 + threadIdx.x; idx < i0 + kPer; idx += blockDim.x) {
-                const int h = idx / D, d = idx % D;
-                const uint32_t row = smem_addr(part + h * (D + 2));
-                float mr[kDecodeClusterSplits], lr[kDecodeClusterSplits], ar[kDecodeClusterSplits];
-                float m = -INFINITY;
-#pragma unroll
-                for (int r = 0; r < kDecodeClusterSplits; ++r) {
-                    mr[r] = ld_peer_f32(row + D * 4, r);
-                    lr[r] = ld_peer_f32(row + (D + 1) * 4, r);
-                    ar[r] = ld_peer_f32(row + d * 4, r);
-                    m = fmaxf(m, mr[r]);
-                }
-                float l = 0.f, acc = 0.f;
-#pragma unroll
-                for (int r = 0; r < kDecodeClusterSplits; ++r) {
-                    const float sc = (mr[r] == -INFINITY) ? 0.f : ex2_approx(mr[r] - m);
-                    l += lr[r] * sc;
-                    acc += ar[r] * sc;
-                }
-                const size_t oi = ((size_t)qrow * Hq + g * G + h) * D + d;
-                if (in_bounds((long long)oi, (long long)total * Hq * D)) out[oi] = __float2bfloat16_rn(acc / l);
-            }
-        }
-        cluster_sync_all();                          // peers' shared memory stays until read
-    }
+    decode_merge<D, G, CLUSTER>(mg, b, qrow, CLUSTER ? (long long)total : (long long)gridDim.z, g, Hkv, split, nsplit,
+                                nsplit_max, out, ws_ml, ws_o);
 }
 
 // Log-sum-exp merge of the splits of each (sequence, kv head) into bf16 out.

@@ -12,7 +12,9 @@
 #include "../../include/swa.h"
 #include "decode_kernel.cuh"
 #include "device_common.cuh"
+#include "evict_kernel.cuh"
 #include "prefill_kernel.cuh"
+#include "q8_kernel.cuh"
 
 namespace {
 
@@ -108,7 +110,16 @@ swa_status_t device_info(DeviceInfo **out) {
                                       swa::DecodeCfg<DD, GG>::SMEM_BYTES));                  \
     SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_decode_kernel<DD, GG, swa::kDecodeWindowCluster>, \
                                       cudaFuncAttributeMaxDynamicSharedMemorySize,           \
-                                      swa::DecodeCfg<DD, GG>::SMEM_BYTES));
+                                      swa::DecodeCfg<DD, GG>::SMEM_BYTES));                  \
+    SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_decode_q8_kernel<DD, GG, swa::kDecodeWindow>, \
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize,           \
+                                      swa::DecodeQ8Cfg<DD, GG>::SMEM_BYTES));                \
+    SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_decode_q8_kernel<DD, GG, swa::kDecodeWindowCluster>, \
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize,           \
+                                      swa::DecodeQ8Cfg<DD, GG>::SMEM_BYTES));                \
+    SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_decode_scores_kernel<DD, GG>,                 \
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize,           \
+                                      swa::DecodeScoresCfg<DD, GG>::SMEM_BYTES));
         SWA_SET_DECODE_ATTR(64, 1) SWA_SET_DECODE_ATTR(64, 2) SWA_SET_DECODE_ATTR(64, 3)
         SWA_SET_DECODE_ATTR(64, 4) SWA_SET_DECODE_ATTR(64, 5) SWA_SET_DECODE_ATTR(64, 6)
         SWA_SET_DECODE_ATTR(64, 7) SWA_SET_DECODE_ATTR(64, 8)
@@ -417,12 +428,13 @@ swa_status_t prefill_impl(const void *q, const void *k, const void *v, void *out
 // H, D], sequence b is rows cu[b]..cu[b+1]-1 (any length; one longer than W
 // leaves its last W positions in the buffer).
 // k_sink / v_sink, S > 0: S-slot sink buffers [B, S, Hkv, D] (fixed-length only).
+// append false: the attention alone (fixed-length only).
 swa_status_t prefill_chunk_impl(const void *q, const void *k, const void *v, void *k_cache,
                                 void *v_cache, const int32_t *start_pos, void *out, int B, int C,
                                 int Hq, int Hkv, int D, int W, float scale,
                                 const swa::RopeTable *rope, const int32_t *cu_seqlens,
                                 cudaStream_t s, void *k_sink = nullptr, void *v_sink = nullptr,
-                                int S = 0) {
+                                int S = 0, bool append = true) {
     if (!q || !k || !v || !k_cache || !v_cache || !start_pos || !out) return SWA_ERR_INVALID_ARG;
     if (S < 0 || (S > 0 && (!k_sink || !v_sink || !aligned16(k_sink) || !aligned16(v_sink) || cu_seqlens)))
         return SWA_ERR_INVALID_ARG;
@@ -483,7 +495,7 @@ swa_status_t prefill_chunk_impl(const void *q, const void *k, const void *v, voi
     }
     swa_status_t e = D == 128 ? launch_prefill<128>(mq, mk, mv, mkc, mvc, mks, mvs, p, dev->sms, s)
                               : launch_prefill<64>(mq, mk, mv, mkc, mvc, mks, mvs, p, dev->sms, s);
-    if (e) return e;
+    if (e || !append) return e;
     // attend first, then write the chunk (its keys already rotated) into the buffer
     if (!cu_seqlens)     // positions below S also go to the sink buffer
         return launch_append(k, v, k_cache, v_cache, start_pos, B, C, Hkv, D, W, dev->sms, nullptr, s,
@@ -564,6 +576,298 @@ swa_status_t decode_impl(const void *q, const void *k_cache, const void *v_cache
         if (reinterpret_cast<uintptr_t>(workspace) & 255u) return SWA_ERR_INVALID_ARG;
     }
     return decode_launch(q, k_cache, v_cache, pos, out, B, Hq, Hkv, D, W, scale, workspace, rope, s);
+}
+
+// ----------------------------------------------------------------- 8-bit rolling cache
+bool misaligned(const void *p, uintptr_t by) { return (reinterpret_cast<uintptr_t>(p) & (by - 1)) != 0; }
+
+// Slots per scale: a power of two that the decode kernel's 16-key blocks divide.
+bool bad_q8_block(int block) { return block != 16 && block != 32 && block != 64 && block != 128; }
+
+swa_status_t q8_cache_checks(const void *k_cache, const void *v_cache, const float *k_scale, const float *v_scale,
+                             const int32_t *pos, int B, int Hkv, int D, int W, int block) {
+    if (!k_cache || !v_cache || !k_scale || !v_scale || !pos) return SWA_ERR_INVALID_ARG;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || misaligned(k_scale, 4) || misaligned(v_scale, 4) ||
+        misaligned(pos, 4))
+        return SWA_ERR_INVALID_ARG;
+    if (B < 1 || W < 1 || Hkv < 1 || bad_q8_block(block)) return SWA_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return SWA_ERR_UNSUPPORTED;
+    if (B > 65535) return SWA_ERR_UNSUPPORTED;
+    return SWA_OK;
+}
+
+template <int BLOCK, int D>
+swa_status_t launch_append_q8(const void *k_new, const void *v_new, void *k_cache, void *v_cache, float *k_scale,
+                              float *v_scale, const int32_t *pos, int B, int T, int Hkv, int W, cudaStream_t s) {
+    const int nblk = (int)(((long long)W + BLOCK - 1) / BLOCK);
+    const int ntouch = swa::q8_blocks_touched(T, BLOCK, nblk);
+    const long long gx = (long long)ntouch * 2 * Hkv;
+    if (gx > 0x7fffffffll) return SWA_ERR_UNSUPPORTED;
+    swa::swa_append_q8_kernel<BLOCK, D><<<dim3((unsigned)gx, B), BLOCK * D / 32, 0, s>>>(
+        static_cast<const uint4 *>(k_new), static_cast<const uint4 *>(v_new), static_cast<uint2 *>(k_cache),
+        static_cast<uint2 *>(v_cache), k_scale, v_scale, pos, T, W, Hkv, nblk, ntouch);
+    SWA_CUDA_TRY(cudaGetLastError());
+    return SWA_OK;
+}
+
+swa_status_t append_q8_impl(const void *k_new, const void *v_new, void *k_cache, void *v_cache, float *k_scale,
+                            float *v_scale, const int32_t *pos, int B, int T, int Hkv, int D, int W, int block,
+                            cudaStream_t s) {
+    if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new)) return SWA_ERR_INVALID_ARG;
+    if (swa_status_t e = q8_cache_checks(k_cache, v_cache, k_scale, v_scale, pos, B, Hkv, D, W, block)) return e;
+    if (T < 1 || T > W) return SWA_ERR_INVALID_ARG;
+#define SWA_APPEND_Q8(BL)                                                                                          \
+    case BL:                                                                                                      \
+        return D == 128 ? launch_append_q8<BL, 128>(k_new, v_new, k_cache, v_cache, k_scale, v_scale, pos, B, T,   \
+                                                    Hkv, W, s)                                                     \
+                        : launch_append_q8<BL, 64>(k_new, v_new, k_cache, v_cache, k_scale, v_scale, pos, B, T,    \
+                                                   Hkv, W, s);
+    switch (block) {
+        SWA_APPEND_Q8(16)
+        SWA_APPEND_Q8(32)
+        SWA_APPEND_Q8(64)
+        SWA_APPEND_Q8(128)
+        default: return SWA_ERR_INVALID_ARG;
+    }
+#undef SWA_APPEND_Q8
+}
+
+template <int D, int G>
+swa_status_t launch_decode_q8_dg(const void *q, const void *kc, const void *vc, const float *ks, const float *vs,
+                                 const int32_t *pos, void *out, int B, int Hkv, int W, int block, float scale,
+                                 void *ws, int kv_rep, cudaStream_t s) {
+    const int nsm = decode_nsplit_max(B, Hkv, W);
+    const int split = decode_split_keys(B, Hkv, W);
+    const bool cluster = nsm == swa::kDecodeClusterSplits;
+    const size_t o_elems = (size_t)B * Hkv * nsm * G * D;
+    float *ws_o = static_cast<float *>(ws);
+    float2 *ws_ml =
+        ws ? reinterpret_cast<float2 *>(static_cast<char *>(ws) + ((o_elems * 4 + 255) & ~size_t(255))) : nullptr;
+    int block_log2 = 0;
+    while ((1 << block_log2) < block) ++block_log2;
+    const int nblk = (int)(((long long)W + block - 1) / block);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(nsm, Hkv, B);
+    cfg.blockDim = dim3(swa::kDecodeWarps * 32);
+    cfg.dynamicSmemBytes = swa::DecodeQ8Cfg<D, G>::SMEM_BYTES;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = swa::kDecodeClusterSplits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster ? 1 : 0;
+    auto kernel = cluster ? swa::swa_decode_q8_kernel<D, G, swa::kDecodeWindowCluster>
+                          : swa::swa_decode_q8_kernel<D, G, swa::kDecodeWindow>;
+    SWA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, static_cast<const __nv_bfloat16 *>(q),
+                                    static_cast<const uint8_t *>(kc), static_cast<const uint8_t *>(vc), ks, vs, pos,
+                                    static_cast<__nv_bfloat16 *>(out), ws_ml, ws_o, Hkv, W, nsm, scale * kLog2e,
+                                    split, kv_rep, block_log2, nblk));
+    if (nsm > 1 && !cluster) {
+        swa::swa_decode_combine_kernel<D, G><<<dim3(Hkv, B), G * D, 0, s>>>(
+            pos, ws_ml, ws_o, static_cast<__nv_bfloat16 *>(out), Hkv, W, nsm, 0, split);
+        SWA_CUDA_TRY(cudaGetLastError());
+    }
+    return SWA_OK;
+}
+
+// One call of LAUNCH<D, G>(args) for a run-time D and G (1..8).
+#define SWA_DISPATCH_DG(LAUNCH, D, G, ...)                                      \
+    switch ((G) + ((D) == 128 ? 8 : 0)) {                                       \
+        case 1: return LAUNCH<64, 1>(__VA_ARGS__);                              \
+        case 2: return LAUNCH<64, 2>(__VA_ARGS__);                              \
+        case 3: return LAUNCH<64, 3>(__VA_ARGS__);                              \
+        case 4: return LAUNCH<64, 4>(__VA_ARGS__);                              \
+        case 5: return LAUNCH<64, 5>(__VA_ARGS__);                              \
+        case 6: return LAUNCH<64, 6>(__VA_ARGS__);                              \
+        case 7: return LAUNCH<64, 7>(__VA_ARGS__);                              \
+        case 8: return LAUNCH<64, 8>(__VA_ARGS__);                              \
+        case 9: return LAUNCH<128, 1>(__VA_ARGS__);                             \
+        case 10: return LAUNCH<128, 2>(__VA_ARGS__);                            \
+        case 11: return LAUNCH<128, 3>(__VA_ARGS__);                            \
+        case 12: return LAUNCH<128, 4>(__VA_ARGS__);                            \
+        case 13: return LAUNCH<128, 5>(__VA_ARGS__);                            \
+        case 14: return LAUNCH<128, 6>(__VA_ARGS__);                            \
+        case 15: return LAUNCH<128, 7>(__VA_ARGS__);                            \
+        case 16: return LAUNCH<128, 8>(__VA_ARGS__);                            \
+        default: return SWA_ERR_UNSUPPORTED;                                    \
+    }
+
+swa_status_t decode_q8_impl(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                            const float *v_scale, const int32_t *pos, void *out, int B, int Hq, int Hkv, int D,
+                            int W, int block, float scale, void *workspace, size_t workspace_bytes, cudaStream_t s) {
+    if (swa_status_t e = decode_checks(q, k_cache, v_cache, pos, out, B, Hq, Hkv, D, W, scale)) return e;
+    if (swa_status_t e = q8_cache_checks(k_cache, v_cache, k_scale, v_scale, pos, B, Hkv, D, W, block)) return e;
+    int rep = 1;
+    const int G = decode_group(Hq, Hkv, &rep);
+    if (decode_nsplit_max(B, Hkv * rep, W) > 1) {
+        if (!workspace || workspace_bytes < decode_workspace_bytes(B, Hq, Hkv, D, W) || misaligned(workspace, 256))
+            return SWA_ERR_INVALID_ARG;
+    }
+    DeviceInfo *dev = nullptr;
+    if (swa_status_t e = device_info(&dev)) return e;
+    SWA_DISPATCH_DG(launch_decode_q8_dg, D, G, q, k_cache, v_cache, k_scale, v_scale, pos, out, B, Hkv * rep, W, block,
+                    scale, workspace, rep, s)
+}
+
+// The widened K and V, each [B, W, Hkv, D] bf16.
+size_t prefill_chunk_q8_workspace_bytes(int B, int Hkv, int D, int W) {
+    if (B < 1 || W < 1 || Hkv < 1 || (D != 64 && D != 128)) return 0;
+    return (size_t)B * W * Hkv * D * 2 * 2;
+}
+
+swa_status_t prefill_chunk_q8_impl(const void *q, const void *k, const void *v, void *k_cache, void *v_cache,
+                                   float *k_scale, float *v_scale, const int32_t *start_pos, void *out, int B, int C,
+                                   int Hq, int Hkv, int D, int W, int block, float scale, void *workspace,
+                                   size_t workspace_bytes, cudaStream_t s) {
+    if (!q || !k || !v || !out || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out))
+        return SWA_ERR_INVALID_ARG;
+    if (swa_status_t e = check_heads(Hq, Hkv, D)) return e;
+    if (swa_status_t e = q8_cache_checks(k_cache, v_cache, k_scale, v_scale, start_pos, B, Hkv, D, W, block)) return e;
+    if (C < 1 || C > W || bad_scale(scale)) return SWA_ERR_INVALID_ARG;
+    if (!workspace || misaligned(workspace, 256) ||
+        workspace_bytes < prefill_chunk_q8_workspace_bytes(B, Hkv, D, W))
+        return SWA_ERR_INVALID_ARG;
+    DeviceInfo *dev = nullptr;
+    if (swa_status_t e = device_info(&dev)) return e;
+    const size_t half = (size_t)B * W * Hkv * D * 2;
+    char *kd = static_cast<char *>(workspace), *vd = kd + half;
+    const int nblk = (int)(((long long)W + block - 1) / block);
+    long long blocks = ((long long)B * W * Hkv * (D / 16) + 255) / 256;
+    if (blocks > (long long)dev->sms * 16) blocks = (long long)dev->sms * 16;
+    swa::swa_widen_q8_kernel<<<(int)blocks, 256, 0, s>>>(
+        static_cast<const uint4 *>(k_cache), static_cast<const uint4 *>(v_cache), k_scale, v_scale, start_pos,
+        reinterpret_cast<uint4 *>(kd), reinterpret_cast<uint4 *>(vd), B, W, Hkv, D / 16, block, nblk);
+    SWA_CUDA_TRY(cudaGetLastError());
+    if (swa_status_t e = prefill_chunk_impl(q, k, v, kd, vd, start_pos, out, B, C, Hq, Hkv, D, W, scale, nullptr,
+                                            nullptr, s, nullptr, nullptr, 0, false))
+        return e;
+    return append_q8_impl(k, v, k_cache, v_cache, k_scale, v_scale, start_pos, B, C, Hkv, D, W, block, s);
+}
+
+// ----------------------------------------------------------------- fixed-size cache with eviction
+// Workspace: partial outputs, then {m, l, l} per partial row, then the scores
+// [B, Hq, M up to a multiple of 16].
+struct ScoresLayout {
+    int nsm, split, stride;
+    size_t ml_off, scores_off, bytes;
+};
+
+ScoresLayout scores_layout(int B, int Hq, int groups, int D, int M) {
+    ScoresLayout l;
+    l.nsm = decode_nsplit_max(B, groups, M);
+    l.split = decode_split_keys(B, groups, M);
+    l.stride = (M + 15) & ~15;
+    const size_t rows = (size_t)B * Hq * l.nsm;
+    l.ml_off = (rows * D * 4 + 255) & ~size_t(255);
+    l.scores_off = (l.ml_off + rows * 16 + 255) & ~size_t(255);
+    l.bytes = l.scores_off + (size_t)B * Hq * l.stride * 4;
+    return l;
+}
+
+constexpr int kMaxFinishHeads = 2048;               // 16 bytes of shared memory each
+
+bool scores_supported(int B, int Hq, int Hkv, int M) {
+    int rep = 1;
+    decode_group(Hq, Hkv, &rep);
+    return B <= 65535 && (long long)Hkv * rep <= 65535 && Hq / Hkv <= kMaxFinishHeads && M <= swa::kEvictMaxSlots;
+}
+
+size_t decode_weights_workspace_bytes(int B, int Hq, int Hkv, int D, int M) {
+    if (B < 1 || M < 1 || check_heads(Hq, Hkv, D) != SWA_OK || !scores_supported(B, Hq, Hkv, M)) return 0;
+    int rep = 1;
+    decode_group(Hq, Hkv, &rep);
+    return scores_layout(B, Hq, Hkv * rep, D, M).bytes;
+}
+
+template <int D, int G>
+swa_status_t launch_decode_weights_dg(const void *q, const void *kc, const void *vc, const int32_t *slot_pos,
+                                      const float *weights, float *weights_out, const int32_t *pos, void *out, int B,
+                                      int groups, int M, float scale, void *ws, int rep, cudaStream_t s) {
+    const ScoresLayout l = scores_layout(B, groups * G, groups, D, M);
+    char *base = static_cast<char *>(ws);
+    float *ws_o = reinterpret_cast<float *>(base);
+    float4 *ws_ml = reinterpret_cast<float4 *>(base + l.ml_off);
+    float *scores = reinterpret_cast<float *>(base + l.scores_off);
+    swa::swa_decode_scores_kernel<D, G>
+        <<<dim3(l.nsm, groups, B), swa::kDecodeWarps * 32, swa::DecodeScoresCfg<D, G>::SMEM_BYTES, s>>>(
+            static_cast<const __nv_bfloat16 *>(q), static_cast<const __nv_bfloat16 *>(kc),
+            static_cast<const __nv_bfloat16 *>(vc), slot_pos, pos, ws_ml, ws_o, scores, l.stride, groups, M, l.nsm,
+            scale * kLog2e, l.split, rep);
+    SWA_CUDA_TRY(cudaGetLastError());
+    const int Hkv = groups / rep, Gall = G * rep;
+    swa::swa_weights_finish_kernel<<<dim3((M + swa::kFinishSlots - 1) / swa::kFinishSlots, Hkv, B),
+                                     swa::kFinishThreads, Gall * sizeof(float4), s>>>(
+        pos, ws_ml, ws_o, scores, l.stride, weights, weights_out, static_cast<__nv_bfloat16 *>(out), Hkv, Gall, rep, D,
+        M, l.nsm, l.split);
+    SWA_CUDA_TRY(cudaGetLastError());
+    return SWA_OK;
+}
+
+swa_status_t decode_weights_impl(const void *q, const void *k_cache, const void *v_cache, const int32_t *slot_pos,
+                                 const float *weights, float *weights_out, const int32_t *pos, void *out, int B,
+                                 int Hq, int Hkv, int D, int M, float scale, void *workspace, size_t workspace_bytes,
+                                 cudaStream_t s) {
+    if (swa_status_t e = decode_checks(q, k_cache, v_cache, pos, out, B, Hq, Hkv, D, M, scale)) return e;
+    if (!slot_pos || !weights_out || misaligned(slot_pos, 4) || misaligned(weights, 4) || misaligned(weights_out, 4))
+        return SWA_ERR_INVALID_ARG;
+    if (!scores_supported(B, Hq, Hkv, M)) return SWA_ERR_UNSUPPORTED;
+    if (!workspace || misaligned(workspace, 256) ||
+        workspace_bytes < decode_weights_workspace_bytes(B, Hq, Hkv, D, M))
+        return SWA_ERR_INVALID_ARG;
+    int rep = 1;
+    const int G = decode_group(Hq, Hkv, &rep);
+    DeviceInfo *dev = nullptr;
+    if (swa_status_t e = device_info(&dev)) return e;
+    SWA_DISPATCH_DG(launch_decode_weights_dg, D, G, q, k_cache, v_cache, slot_pos, weights, weights_out, pos, out, B,
+                    Hkv * rep, M, scale, workspace, rep, s)
+}
+
+// Sizes of a fixed-size cache: M slots of which S sinks and R recent ones
+// (the newest among them) are never evicted.
+swa_status_t budget_checks(int B, int Hkv, int D, int M, int S, int R) {
+    if (B < 1 || Hkv < 1 || M < 1 || S < 0 || R < 1 || (long long)S + R > M) return SWA_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return SWA_ERR_UNSUPPORTED;
+    if (B > 65535 || M > swa::kEvictMaxSlots) return SWA_ERR_UNSUPPORTED;
+    return SWA_OK;
+}
+
+swa_status_t evict_append_impl(const void *k_new, const void *v_new, void *k_cache, void *v_cache, int32_t *slot_pos,
+                               float *weights, const int32_t *pos, int32_t *slots, int B, int Hkv, int D, int M, int S,
+                               int R, cudaStream_t s) {
+    if (!k_new || !v_new || !k_cache || !v_cache || !slot_pos || !weights || !pos) return SWA_ERR_INVALID_ARG;
+    if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        misaligned(slot_pos, 4) || misaligned(weights, 4) || misaligned(pos, 4) || misaligned(slots, 4))
+        return SWA_ERR_INVALID_ARG;
+    if (swa_status_t e = budget_checks(B, Hkv, D, M, S, R)) return e;
+    swa::swa_evict_append_kernel<<<dim3(Hkv, B), swa::kEvictThreads, 0, s>>>(
+        static_cast<const uint4 *>(k_new), static_cast<const uint4 *>(v_new), static_cast<uint4 *>(k_cache),
+        static_cast<uint4 *>(v_cache), slot_pos, weights, pos, slots, Hkv, M, D / 8, S, R);
+    SWA_CUDA_TRY(cudaGetLastError());
+    return SWA_OK;
+}
+
+swa_status_t keep_impl(const void *k, const void *v, const float *weights, const int32_t *lens, void *k_cache,
+                       void *v_cache, int32_t *slot_pos, float *weights_out, int B, int N, int Hkv, int D, int M,
+                       int S, int R, cudaStream_t s) {
+    if (!k || !v || !weights || !lens || !k_cache || !v_cache || !slot_pos || !weights_out) return SWA_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) || misaligned(weights, 4) ||
+        misaligned(lens, 4) || misaligned(slot_pos, 4) || misaligned(weights_out, 4) || N < 1)
+        return SWA_ERR_INVALID_ARG;
+    if (swa_status_t e = budget_checks(B, Hkv, D, M, S, R)) return e;
+    DeviceInfo *dev = nullptr;
+    if (swa_status_t e = device_info(&dev)) return e;
+    swa::swa_keep_select_kernel<<<dim3(Hkv, B), swa::kKeepThreads, swa::kKeepSmem, s>>>(
+        weights, lens, slot_pos, weights_out, N, Hkv, M, S, R);
+    SWA_CUDA_TRY(cudaGetLastError());
+    long long blocks = ((long long)B * M * Hkv * (D / 8) + 255) / 256;
+    if (blocks > (long long)dev->sms * 16) blocks = (long long)dev->sms * 16;
+    swa::swa_keep_copy_kernel<<<(int)blocks, 256, 0, s>>>(
+        static_cast<const uint4 *>(k), static_cast<const uint4 *>(v), slot_pos, static_cast<uint4 *>(k_cache),
+        static_cast<uint4 *>(v_cache), B, N, Hkv, M, D / 8);
+    SWA_CUDA_TRY(cudaGetLastError());
+    return SWA_OK;
 }
 
 }  // namespace
@@ -742,6 +1046,58 @@ swa_status_t swa_decode_sinks(const void *q, const void *k_cache, const void *v_
                                            nullptr, s, k_sink, v_sink, S)
                     : launch_decode_d<64>(G, rep, q, k_cache, v_cache, pos, out, B, Hkv * rep, W, scale, workspace,
                                           nullptr, s, k_sink, v_sink, S);
+}
+
+swa_status_t swa_cache_append_q8(const void *k_new, const void *v_new, void *k_cache, void *v_cache, float *k_scale,
+                                 float *v_scale, const int32_t *pos, int B, int T, int Hkv, int D, int W, int block,
+                                 swa_stream_t stream) {
+    return append_q8_impl(k_new, v_new, k_cache, v_cache, k_scale, v_scale, pos, B, T, Hkv, D, W, block,
+                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+swa_status_t swa_decode_q8(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                           const float *v_scale, const int32_t *pos, void *out, int B, int Hq, int Hkv, int D, int W,
+                           int block, float scale, void *workspace, size_t workspace_bytes, swa_stream_t stream) {
+    return decode_q8_impl(q, k_cache, v_cache, k_scale, v_scale, pos, out, B, Hq, Hkv, D, W, block, scale, workspace,
+                          workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t swa_prefill_chunk_q8_workspace_size(int B, int Hkv, int D, int W) {
+    return prefill_chunk_q8_workspace_bytes(B, Hkv, D, W);
+}
+
+swa_status_t swa_prefill_chunk_q8(const void *q, const void *k, const void *v, void *k_cache, void *v_cache,
+                                  float *k_scale, float *v_scale, const int32_t *start_pos, void *out, int B, int C,
+                                  int Hq, int Hkv, int D, int W, int block, float scale, void *workspace,
+                                  size_t workspace_bytes, swa_stream_t stream) {
+    return prefill_chunk_q8_impl(q, k, v, k_cache, v_cache, k_scale, v_scale, start_pos, out, B, C, Hq, Hkv, D, W,
+                                 block, scale, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t swa_decode_weights_workspace_size(int B, int Hq, int Hkv, int D, int M) {
+    return decode_weights_workspace_bytes(B, Hq, Hkv, D, M);
+}
+
+swa_status_t swa_decode_weights(const void *q, const void *k_cache, const void *v_cache, const int32_t *slot_pos,
+                                const float *weights, float *weights_out, const int32_t *pos, void *out, int B, int Hq,
+                                int Hkv, int D, int M, float scale, void *workspace, size_t workspace_bytes,
+                                swa_stream_t stream) {
+    return decode_weights_impl(q, k_cache, v_cache, slot_pos, weights, weights_out, pos, out, B, Hq, Hkv, D, M, scale,
+                               workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+swa_status_t swa_cache_evict_append(const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+                                    int32_t *slot_pos, float *weights, const int32_t *pos, int32_t *slots, int B,
+                                    int Hkv, int D, int M, int S, int R, swa_stream_t stream) {
+    return evict_append_impl(k_new, v_new, k_cache, v_cache, slot_pos, weights, pos, slots, B, Hkv, D, M, S, R,
+                             reinterpret_cast<cudaStream_t>(stream));
+}
+
+swa_status_t swa_cache_keep(const void *k, const void *v, const float *weights, const int32_t *lens, void *k_cache,
+                            void *v_cache, int32_t *slot_pos, float *weights_out, int B, int N, int Hkv, int D, int M,
+                            int S, int R, swa_stream_t stream) {
+    return keep_impl(k, v, weights, lens, k_cache, v_cache, slot_pos, weights_out, B, N, Hkv, D, M, S, R,
+                     reinterpret_cast<cudaStream_t>(stream));
 }
 
 swa_status_t swa_get_device_status(swa_stream_t stream) {
