@@ -401,6 +401,24 @@ swa_status_t swa_decode_weights(const void *q, const void *k_cache, const void *
                                 swa_stream_t stream);
 size_t swa_decode_weights_workspace_size(int B, int Hq, int Hkv, int D, int M);
 
+/* swa_prefill_weights -- the softmax weight that each key of a prompt receives
+ * from the prompt's last T queries, summed over them and over the query heads
+ * of the group:
+ *   q : [B, T, Hq, D], row t of sequence b at position lens[b] - T + t (rows at
+ *       negative positions count for nothing)      k : [B, N, Hkv, D]
+ *   lens : int32 [B], the prompts' lengths, 0 .. N
+ *   weights[b,g,j] = sum_h sum_t softmax_j(scale * <q[b,t,h], k[b,j,g]>), float32
+ *       [B, Hkv, N], over the window i-W < j <= i of each query; W >= N is dense
+ *       causal.  0 for j >= lens[b].
+ * T from 1 (the last query alone) to N (all of them).  A length outside [0, N]
+ * is recorded as SWA_ERR_INVALID_ARG and gives zeros.  At most 128 query heads
+ * to a KV head.  workspace: at least swa_prefill_weights_workspace_size()
+ * bytes, 256-byte aligned, as for swa_decode. */
+swa_status_t swa_prefill_weights(const void *q, const void *k, const int32_t *lens, float *weights,
+                                 int B, int T, int N, int Hq, int Hkv, int D, int W, float scale,
+                                 void *workspace, size_t workspace_bytes, swa_stream_t stream);
+size_t swa_prefill_weights_workspace_size(int B, int T, int N, int Hq, int Hkv, int D, int W);
+
 /* swa_cache_keep -- cut prompts of lens[b] positions (int32 [B], 0 .. N), k, v
  * [B, N, Hkv, D] with weights float32 [B, Hkv, N], to the M slots of a cache:
  * every position if lens[b] <= M; else the first S, the last R and, of the

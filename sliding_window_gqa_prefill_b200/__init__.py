@@ -25,7 +25,8 @@ __all__ = [
     "SWA_ERR_UNSUPPORTED", "SWA_ERR_CUDA", "SWA_ERR_TIMEOUT", "SWA_WINDOW_EXCL_LEFT",
     "SWA_WINDOW_INCL_LEFT", "bounds_checked", "swa_cache_append_q8", "swa_decode_q8", "swa_prefill_chunk_q8",
     "swa_prefill_chunk_q8_workspace_size", "swa_cache_evict_append", "swa_decode_weights",
-    "swa_decode_weights_workspace_size", "swa_cache_keep",
+    "swa_decode_weights_workspace_size", "swa_cache_keep", "swa_prefill_weights",
+    "swa_prefill_weights_workspace_size",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -37,7 +38,8 @@ DEBUG_LIB_PATH = os.path.join(_PKG, "libswa_debug.so")
 HEADER = os.path.join(_ROOT, "include", "swa.h")
 _SOURCES = [os.path.join(_PKG, "csrc", f) for f in
             ("swa_api.cu", "device_common.cuh", "prefill_plan.cuh", "prefill_kernel.cuh", "decode_kernel.cuh",
-             "q8_kernel.cuh", "evict_kernel.cuh")]
+             "q8_kernel.cuh", "evict_kernel.cuh", "weights_plan.cuh",
+             "weights_kernel.cuh")]
 
 SWA_OK, SWA_ERR_INVALID_ARG, SWA_ERR_UNSUPPORTED, SWA_ERR_CUDA, SWA_ERR_TIMEOUT = 0, 1, 2, 3, 4
 SWA_WINDOW_EXCL_LEFT, SWA_WINDOW_INCL_LEFT = 0, 1
@@ -137,6 +139,10 @@ def lib() -> ctypes.CDLL:
             L.swa_cache_evict_append.argtypes = [vp] * 8 + [i] * 6 + [st]
             L.swa_decode_weights.argtypes = [vp] * 8 + [i] * 5 + [f, vp, z, st]
             L.swa_cache_keep.argtypes = [vp] * 8 + [i] * 7 + [st]
+            L.swa_prefill_weights.argtypes = [vp] * 4 + [i] * 7 + [f, vp, z, st]
+            L.swa_prefill_weights.restype = ctypes.c_int
+            L.swa_prefill_weights_workspace_size.argtypes = [i] * 7
+            L.swa_prefill_weights_workspace_size.restype = z
             for fn in (L.swa_cache_append_q8, L.swa_decode_q8, L.swa_prefill_chunk_q8, L.swa_cache_evict_append,
                        L.swa_decode_weights, L.swa_cache_keep):
                 fn.restype = ctypes.c_int
@@ -608,6 +614,31 @@ def swa_decode_weights(q, k_cache, v_cache, slot_pos, weights, pos, scale: float
                                 _ptr(pos, "pos", torch.int32, (B,), dev), _ptr(out, "out", bf16, rows, dev), B, Hq, Hkv,
                                 D, M, scale, ws, size, _stream_handle(stream)), "swa_decode_weights")
     return out, weights_out
+
+
+def swa_prefill_weights_workspace_size(B: int, T: int, N: int, Hq: int, Hkv: int, D: int, W: int) -> int:
+    return int(lib().swa_prefill_weights_workspace_size(B, T, N, Hq, Hkv, D, W))
+
+
+def swa_prefill_weights(q, k, lens, W: int, scale: float, weights=None, workspace=None, stream=None):
+    """The softmax weight each key of a prompt receives from its last T queries,
+    summed over them and over the group's heads: q [B,T,Hq,D] (row t at position
+    lens[b]-T+t), k [B,N,Hkv,D] bf16, lens int32 [B] -> weights [B,Hkv,N] float32."""
+    import torch
+    dev = torch.cuda.current_device()
+    rows, keys = _dims(q, "q", 4), _dims(k, "k", 4)
+    T, Hq = rows[1], rows[2]
+    B, N, Hkv, D = keys
+    args = (_ptr(q, "q", torch.bfloat16, (B, T, Hq, D), dev), _ptr(k, "k", torch.bfloat16, keys, dev),
+            _ptr(lens, "lens", torch.int32, (B,), dev))
+    if weights is None:
+        weights = _empty((B, Hkv, N), torch.float32, stream)
+    L = lib()
+    W = min(W, N)
+    workspace, ws, size = _scratch(workspace, L.swa_prefill_weights_workspace_size(B, T, N, Hq, Hkv, D, W), dev, stream)
+    _check(L.swa_prefill_weights(*args, _ptr(weights, "weights", torch.float32, (B, Hkv, N), dev), B, T, N, Hq, Hkv, D,
+                                 W, scale, ws, size, _stream_handle(stream)), "swa_prefill_weights")
+    return weights
 
 
 def swa_cache_keep(k, v, weights, lens, k_cache, v_cache, slot_pos, weights_out, S: int, R: int, stream=None) -> None:

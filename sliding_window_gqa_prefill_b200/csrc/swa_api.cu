@@ -15,6 +15,7 @@
 #include "evict_kernel.cuh"
 #include "prefill_kernel.cuh"
 #include "q8_kernel.cuh"
+#include "weights_kernel.cuh"
 
 namespace {
 
@@ -56,13 +57,14 @@ EncodeTiledFn encode_fn() {
 // bf16 tensor [d3, d2, d1, d0] (d0 innermost, contiguous) as a 4-D TMA map
 // with a (64, 1, 128, 1) box and 128-byte swizzle: one 128-row x 128-byte
 // region of a K-major UMMA operand per load.  Out-of-range rows read as zero.
+// box1 x box2 rows: of box1 heads and box2 positions, position-major.
 swa_status_t make_operand_map(CUtensorMap *map, const void *base, uint64_t d0, uint64_t d1,
-                              uint64_t d2, uint64_t d3) {
+                              uint64_t d2, uint64_t d3, uint32_t box1 = 1, uint32_t box2 = 128) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return cuda_fail(cudaErrorNotSupported);
     const cuuint64_t dims[4] = {d0, d1, d2, d3};
     const cuuint64_t strides[3] = {d0 * 2, d0 * d1 * 2, d0 * d1 * d2 * 2};   // bytes, dims 1..3
-    const cuuint32_t box[4] = {64, 1, 128, 1};
+    const cuuint32_t box[4] = {64, box1, box2, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims,
                     strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -98,6 +100,13 @@ swa_status_t device_info(DeviceInfo **out) {
         SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_prefill_kernel<128>,
                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           swa::PrefillCfg<128>::SMEM_ALLOC));
+#define SWA_SET_WEIGHTS_ATTR(DD, PP)                                                          \
+    SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_prefill_weights_kernel<DD, PP>,               \
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize,           \
+                                      swa::WeightsCfg<DD, PP>::SMEM_ALLOC));
+        SWA_SET_WEIGHTS_ATTR(64, 1) SWA_SET_WEIGHTS_ATTR(64, 2)
+        SWA_SET_WEIGHTS_ATTR(128, 1) SWA_SET_WEIGHTS_ATTR(128, 2)
+#undef SWA_SET_WEIGHTS_ATTR
 #define SWA_SET_DECODE_ATTR(DD, GG)                                                           \
     SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_decode_kernel<DD, GG, swa::kDecodeWindow>,    \
                                       cudaFuncAttributeMaxDynamicSharedMemorySize,           \
@@ -870,6 +879,110 @@ swa_status_t keep_impl(const void *k, const void *v, const float *weights, const
     return SWA_OK;
 }
 
+// ----------------------------------------------------------------- weights of a prompt
+// Sizes and workspace of swa_prefill_weights: pass 1's partial results, lse,
+// pass 2's partial results.  The streamed tiles of a unit are split when the
+// units alone would not give kWeightsUnits (two for each SM), down to 4 tiles.
+// A function of the sizes only, as the workspace size is.
+struct WeightsLayout {
+    int G, TQ, nqt, nkt, splits1, splits2;
+    long long units1, units2;
+    size_t lse_off, part_off, bytes;
+};
+
+constexpr long long kWeightsUnits = 296;
+
+int weights_splits(long long units, long long tiles) {
+    long long want = (kWeightsUnits + units - 1) / units;
+    if (want > tiles / 4) want = tiles / 4;
+    return (int)(want < 1 ? 1 : want > 64 ? 64 : want);
+}
+
+WeightsLayout weights_layout(int B, int T, int N, int Hq, int Hkv, int W) {
+    WeightsLayout l;
+    l.G = Hq / Hkv;
+    l.TQ = 128 / l.G;
+    l.nqt = (int)(((long long)T + l.TQ - 1) / l.TQ);
+    l.nkt = (int)(((long long)N + 127) / 128);
+    const long long weff = W < N ? W : N;
+    const long long t1 = (weff + l.TQ - 2) / 128 + 2, t2 = (weff + 126) / l.TQ + 2;
+    const long long bh = (long long)B * Hkv;
+    l.splits1 = weights_splits(bh * l.nqt, t1 < l.nkt ? t1 : l.nkt);
+    l.splits2 = weights_splits(bh * l.nkt, t2 < l.nqt ? t2 : l.nqt);
+    l.units1 = bh * l.nqt * l.splits1;
+    l.units2 = bh * l.nkt * l.splits2;
+    const size_t rows = (size_t)bh * l.nqt * 128;
+    l.lse_off = rows * 2 * l.splits1 * 8;
+    l.part_off = (l.lse_off + rows * 4 + 255) & ~size_t(255);
+    l.bytes = l.part_off + (size_t)2 * l.splits2 * bh * N * 4;
+    return l;
+}
+
+swa_status_t prefill_weights_sizes(int B, int T, int N, int Hq, int Hkv, int D, int W) {
+    if (B < 1 || T < 1 || N < 1 || T > N || W < 1) return SWA_ERR_INVALID_ARG;
+    if (swa_status_t e = check_heads(Hq, Hkv, D)) return e;
+    if (Hq / Hkv > 128) return SWA_ERR_UNSUPPORTED;          // a query tile holds a position's whole group
+    const WeightsLayout l = weights_layout(B, T, N, Hq, Hkv, W);
+    if (l.units1 > 0x7fffffffll || l.units2 > 0x7fffffffll) return SWA_ERR_UNSUPPORTED;
+    return SWA_OK;
+}
+
+template <int D, int PASS>
+swa_status_t launch_weights_pass(const CUtensorMap &mq, const CUtensorMap &mk, const swa::WeightsParams &p, int sms,
+                                 cudaStream_t s) {
+    const int grid = p.num_units < sms ? p.num_units : sms;
+    swa::swa_prefill_weights_kernel<D, PASS>
+        <<<grid, swa::WeightsCfg<D, PASS>::THREADS, swa::WeightsCfg<D, PASS>::SMEM_ALLOC, s>>>(mq, mk, p);
+    SWA_CUDA_TRY(cudaGetLastError());
+    return SWA_OK;
+}
+
+swa_status_t prefill_weights_impl(const void *q, const void *k, const int32_t *lens, float *weights, int B, int T,
+                                  int N, int Hq, int Hkv, int D, int W, float scale, void *workspace,
+                                  size_t workspace_bytes, cudaStream_t s) {
+    if (!q || !k || !lens || !weights || !aligned16(q) || !aligned16(k) || misaligned(lens, 4) ||
+        misaligned(weights, 4) || bad_scale(scale))
+        return SWA_ERR_INVALID_ARG;
+    if (swa_status_t e = prefill_weights_sizes(B, T, N, Hq, Hkv, D, W)) return e;
+    const WeightsLayout l = weights_layout(B, T, N, Hq, Hkv, W);
+    if (!workspace || misaligned(workspace, 256) || workspace_bytes < l.bytes) return SWA_ERR_INVALID_ARG;
+    DeviceInfo *dev = nullptr;
+    if (swa_status_t e = device_info(&dev)) return e;
+    CUtensorMap mq, mk;
+    if (swa_status_t e = make_operand_map(&mq, q, D, Hq, T, B, l.G, l.TQ)) return e;
+    if (swa_status_t e = make_operand_map(&mk, k, D, Hkv, N, B)) return e;
+    char *ws = static_cast<char *>(workspace);
+    float *lse = reinterpret_cast<float *>(ws + l.lse_off), *part = reinterpret_cast<float *>(ws + l.part_off);
+    swa::WeightsParams p{};
+    p.B = B, p.N = N, p.T = T, p.Hkv = Hkv, p.G = l.G, p.TQ = l.TQ;
+    p.W = W < N ? W : N;
+    p.nqt = l.nqt, p.nkt = l.nkt;
+    p.scale_log2 = scale * kLog2e;
+    p.lens = lens;
+    p.ml = reinterpret_cast<float2 *>(ws);
+    p.lse = lse;
+    p.part = part;
+    p.splits = l.splits1;
+    p.num_units = (int)l.units1;
+    if (swa_status_t e = D == 128 ? launch_weights_pass<128, 1>(mq, mk, p, dev->sms, s)
+                                  : launch_weights_pass<64, 1>(mq, mk, p, dev->sms, s))
+        return e;
+    swa::swa_weights_lse_kernel<<<(unsigned)((long long)B * Hkv * l.nqt), 128, 0, s>>>(
+        p.ml, lse, lens, N, T, Hkv, l.G, l.TQ, l.nqt, 2 * l.splits1);
+    SWA_CUDA_TRY(cudaGetLastError());
+    p.splits = l.splits2;
+    p.num_units = (int)l.units2;
+    if (swa_status_t e = D == 128 ? launch_weights_pass<128, 2>(mq, mk, p, dev->sms, s)
+                                  : launch_weights_pass<64, 2>(mq, mk, p, dev->sms, s))
+        return e;
+    const long long n = (long long)B * Hkv * N;
+    long long blocks = (n + 255) / 256;
+    if (blocks > (long long)dev->sms * 16) blocks = (long long)dev->sms * 16;
+    swa::swa_weights_sum_kernel<<<(int)blocks, 256, 0, s>>>(part, weights, n, 2 * l.splits2);
+    SWA_CUDA_TRY(cudaGetLastError());
+    return SWA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1098,6 +1211,17 @@ swa_status_t swa_cache_keep(const void *k, const void *v, const float *weights, 
                             int S, int R, swa_stream_t stream) {
     return keep_impl(k, v, weights, lens, k_cache, v_cache, slot_pos, weights_out, B, N, Hkv, D, M, S, R,
                      reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t swa_prefill_weights_workspace_size(int B, int T, int N, int Hq, int Hkv, int D, int W) {
+    return prefill_weights_sizes(B, T, N, Hq, Hkv, D, W) == SWA_OK ? weights_layout(B, T, N, Hq, Hkv, W).bytes : 0;
+}
+
+swa_status_t swa_prefill_weights(const void *q, const void *k, const int32_t *lens, float *weights, int B, int T,
+                                 int N, int Hq, int Hkv, int D, int W, float scale, void *workspace,
+                                 size_t workspace_bytes, swa_stream_t stream) {
+    return prefill_weights_impl(q, k, lens, weights, B, T, N, Hq, Hkv, D, W, scale, workspace, workspace_bytes,
+                                reinterpret_cast<cudaStream_t>(stream));
 }
 
 swa_status_t swa_get_device_status(swa_stream_t stream) {

@@ -104,3 +104,15 @@ def test_binding_refuses_what_is_not_a_cuda_tensor_of_the_right_kind(monkeypatch
         swa.swa_decode_weights(k[:, 0], k, k, s, s, None, 0.1)
     with pytest.raises(TypeError, match="CUDA tensor"):
         swa.swa_cache_keep(k, k, s, None, k, k, s, s, 1, 2)
+
+
+def test_prefill_weights(lib):
+    #        q  k  lens w  B  T  N   Hq Hkv D  W   scale ws bytes stream
+    good = [P] * 4 + [1, 8, 100, 4, 2, 64, 100, 0.1, P, 1 << 30, None]
+    vary(lib.swa_prefill_weights, good, [({0: None}, BAD), ({1: None}, BAD), ({2: None}, BAD), ({3: None}, BAD)] + [
+        ({0: P + 2}, BAD), ({1: P + 8}, BAD), ({2: P + 1}, BAD), ({3: P + 2}, BAD), ({4: 0}, BAD), ({5: 0}, BAD),
+        ({5: 101}, BAD), ({6: 0}, BAD), ({7: 3}, BAD), ({8: 0}, BAD), ({9: 96}, UNSUP), ({10: 0}, BAD), ({11: 0.0}, BAD),
+        ({11: float("nan")}, BAD), ({12: None}, BAD), ({12: P + 16}, BAD), ({13: 16}, BAD), ({7: 258}, UNSUP)])
+    size = lib.swa_prefill_weights_workspace_size
+    assert size(1, 8, 100, 4, 2, 64, 100) > 0
+    assert size(1, 101, 100, 4, 2, 64, 100) == size(1, 8, 100, 3, 2, 64, 100) == size(1, 8, 100, 258, 2, 64, 100) == 0
