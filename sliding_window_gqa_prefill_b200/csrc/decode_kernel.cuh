@@ -127,21 +127,21 @@ __device__ __forceinline__ uint32_t swz_off(int r, int ch, int row_bytes) {
 // the blocks of the cluster too (each merges and writes a quarter of the
 // outputs); else writes the output if the window is one split, and the split's
 // partial result to the workspace if it is not.  out_rows: rows of out.
-template <int D, int G, bool CLUSTER>
+template <int D, int G, bool CLUSTER, int WARPS = kDecodeWarps>
 __device__ __forceinline__ void decode_merge(float *mg, int b, int qrow, long long out_rows, int g, int Hkv, int split,
                                              int nsplit, int nsplit_max, __nv_bfloat16 *out, float2 *ws_ml,
                                              float *ws_o) {
     const int Hq = Hkv * G;
     __syncthreads();
-    float *part = mg + kDecodeWarps * G * (D + 2);  // [G][D+2]: the block's merge (cluster modes)
+    float *part = mg + WARPS * G * (D + 2);  // [G][D+2]: the block's merge (cluster modes)
     for (int idx = threadIdx.x; idx < G * D; idx += blockDim.x) {
         const int h = idx / D, d = idx % D;
         float m = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kDecodeWarps; ++w) m = fmaxf(m, mg[(w * G + h) * (D + 2) + D]);
+        for (int w = 0; w < WARPS; ++w) m = fmaxf(m, mg[(w * G + h) * (D + 2) + D]);
         float l = 0.f, acc = 0.f;
 #pragma unroll
-        for (int w = 0; w < kDecodeWarps; ++w) {
+        for (int w = 0; w < WARPS; ++w) {
             const float *src = mg + (w * G + h) * (D + 2);
             const float sc = (src[D] == -INFINITY) ? 0.f : ex2_approx(src[D] - m);
             l += src[D + 1] * sc;

@@ -248,49 +248,67 @@ __global__ void swa_widen_q8_kernel(const uint4 *__restrict__ k_cache, const uin
 // Decode over the 8-bit buffer: out = sum_j softmax_j(scale q.k_j) v_j over
 // the slots 0 .. min(pos+1, W)-1, as swa_decode_kernel, at half its bytes.
 //
-// Arithmetic.  Codes widen exactly to f16, so both products run as f16
-// tensor-core tiles (mma.sync m16n8k16) on unrounded codes, with the block
-// scales applied in fp32 afterwards:
-//  * S = (q 2^-x) . c_k, times scale 2^x s_k.  x brings each head's largest
-//    |q| to [2^14, 2^15): q rounds in f16 only below 2^-28 of that;
-//  * O += s_v (P . c_v): the product of one 16-key block starts from zero and
-//    joins O by one fp32 FMA with the block's scale;
+// Arithmetic, per 16 keys and warp (G query heads of the group, at most 8):
+//  * S = Q K^T on the codes themselves (mma.sync m16n8k32, e4m3): q, brought by a
+//    power of two to a largest magnitude in [2^7, 2^8), is the sum of two e4m3
+//    numbers, hi + lo / 16, exactly but for what lies below 2^-21 of that
+//    largest element (a bf16 has 8 significant bits, e4m3 two times 4).  hi are
+//    rows 0..7 of the 16-row tile, lo rows 8..15, so the split costs nothing.
+//    The K scale, the softmax scale and the power of two are one fp32 factor.
 //  * P is rounded to f16 (2^-11 relative; bf16's 2^-8 in the 16-bit cache's
-//    kernel) and l sums it as rounded.  P is 2^7 larger than 2^(s - offset),
-//    at most 2^15, so weights down to 2^-21 of the largest keep all their bits
-//    and those down to 2^-31 some: a long tail of small weights is not lost.
-// The order of d inside a product is free as long as q and k agree, and the
-// order of the output columns is free until they are written; both are chosen
-// so that a lane's fragment is 16 consecutive codes of one row: K is read by
-// one 16-byte shared load per row and half, V by one per key, and the bytes
-// of two keys are interleaved with byte permutes.
+//    kernel) and l sums it as rounded.  P is 2^7 larger than 2^(s - offset), at
+//    most 2^15, so weights down to 2^-21 of the largest keep all their bits and
+//    those down to 2^-31 some: a long tail of small weights is not lost, as it
+//    would be in 8 bits.
+//  * O^T = V^T P^T (mma.sync m16n8k16, f16): V^T as the 16-row operand fills the
+//    tile (16 columns of d by 16 keys), and the P of a lane is its fragment of
+//    P^T as it stands.  Codes widen exactly to f16; the product of 16 keys starts
+//    from zero and joins O by one fp32 FMA with the block's scale.
+// The order of d inside a product is free as long as both operands agree, and
+// the order of O's rows is free until they are written; both are chosen so that
+// a lane's fragments are 16 consecutive codes of one row: K is read by one
+// 16-byte shared load per row and half, V by one per key, and the bytes of two
+// keys are paired by byte permutes.
+//
+// Measured at B=64, W=4096, 32 / 8 heads, D=128: 99 to 101 us, 5.4 TB/s.  With
+// both products in f16 and the heads as rows of both it took 114 to 142 us (the
+// 16-bit copies of K cost registers, and the O product half its rows); with K
+// alone in f16 104 us.  Four blocks of four warps to an SM, 3 stages of 16 keys:
+// two blocks with more stages 117 to 121 us, stages of 32 keys 100 us.
+//
+// The codes of kQ8Stage keys come into a warp's own ring as two TMA boxes (rows
+// of one head, K and V) that one lane issues, so copying costs the warp a
+// handful of instructions.
+constexpr int kQ8Stage = 16;           // keys per TMA box
+constexpr int kQ8Warps = 4;
+
 template <int D, int G>
 struct DecodeQ8Cfg {
     static constexpr int CH = D / 16;                          // 16-byte chunks per key row
-    static constexpr int BLK_BYTES = kDecodeBlk * D;           // K (or V) codes of one 16-key block
-    static constexpr int STAGE_BYTES = 2 * BLK_BYTES;
-    static constexpr int STAGES = 6;                           // 16-key blocks in flight per warp
+    static constexpr int TILE_BYTES = kQ8Stage * D;            // K (or V) codes of one stage
+    static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
+    static constexpr int STAGES = 3;
     static constexpr int WARP_RING = STAGES * STAGE_BYTES;
-    static constexpr int RING_BYTES = kDecodeWarps * WARP_RING;
-    static constexpr int CPL = kDecodeBlk * CH / 32;           // 16-byte copies per lane, K or V
-    static constexpr int KSTEPS = D / 16;
-    static constexpr int NB = D / 8;
-    static constexpr int MERGE_BYTES = (kDecodeWarps + 1) * G * (D + 2) * 4;
-    static constexpr int SMEM_BYTES = RING_BYTES > MERGE_BYTES ? RING_BYTES : MERGE_BYTES;
+    static constexpr int RING_BYTES = kQ8Warps * WARP_RING;
+    static constexpr int KSTEPS = D / 32;                      // MMA k-steps of S
+    static constexpr int MT = D / 16;                          // 16-row tiles of O^T
+    static constexpr int MERGE_BYTES = (kQ8Warps + 1) * G * (D + 2) * 4;
+    static constexpr int OFF_BAR = RING_BYTES > MERGE_BYTES ? RING_BYTES : MERGE_BYTES;
+    static constexpr int OFF_ABORT = OFF_BAR + kQ8Warps * STAGES * 8;
+    static constexpr int SMEM_BYTES = OFF_ABORT + 8 + 1024;    // slack for 1024-byte alignment
     static_assert(D == 64 || D == 128, "head_dim");
     static_assert(G >= 1 && G <= 8, "group size 1 to 8 (the rows 0..7 of the MMA tile)");
-    static_assert(CPL * 32 == kDecodeBlk * CH, "copies per lane");
+    static_assert(OFF_BAR % 8 == 0, "barrier alignment");
 };
 
-// Shared-memory offset of 16-byte chunk `ch` of code row `r`.  A line of 128
-// bytes (one row of D = 128, two of D = 64) has its 8 chunks permuted by XOR
-// so that the eight lanes of a phase hit eight different 16-byte bank groups
-// both when they read 2 rows x 4 chunks (K) and 4 rows, two apart, x 2 chunks
-// (V).
+// Shared-memory offset of 16-byte chunk `ch` of code row `r`, as TMA places it:
+// 128-byte swizzle for D = 128 (chunk ^ row mod 8), 64-byte for D = 64 (chunk ^
+// (row / 2) mod 4).  The V loads of a phase (4 rows, two apart, x 2 chunks) and
+// the K loads (2 rows x 4 chunks) meet at most two to a bank.
 template <int D>
 __device__ __forceinline__ uint32_t q8_off(int r, int ch) {
-    if (D == 128) return (uint32_t)(r * 128 + ((ch ^ (((r >> 1) & 3) << 1) ^ ((r & 1) << 2)) << 4));
-    return (uint32_t)((r >> 1) * 128 + (((((r & 1) << 2) | ch) ^ (((r >> 1) & 3) << 1)) << 4));
+    if (D == 128) return (uint32_t)(r * 128 + ((ch ^ (r & 7)) << 4));
+    return (uint32_t)(r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -308,29 +326,38 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     return v;
 }
 
-// As mma_rows8, f16 operands: rows 0..7 of the tile only.
-__device__ __forceinline__ void mma_rows8_f16(float &d0, float &d1, uint32_t a0, uint32_t a2, uint32_t b0,
-                                              uint32_t b1) {
-    [[maybe_unused]] float u2, u3;
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%10, %11, %12, %13};"
-        : "=f"(d0), "=f"(d1), "=f"(u2), "=f"(u3)
-        : "r"(a0), "r"(0u), "r"(a2), "r"(0u), "r"(b0), "r"(b1), "f"(d0), "f"(d1), "f"(0.f), "f"(0.f));
+// D(16x8, fp32) += A(16x32, e4m3) B(32x8, e4m3), warp-wide.
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A(16x16, f16) B(16x8, f16), warp-wide, fp32.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // MODE kDecodeWindow (splits merged by swa_decode_combine_kernel) or
 // kDecodeWindowCluster (the splits of a window are the blocks of a cluster).
 template <int D, int G, int MODE>
-__global__ void __launch_bounds__(kDecodeWarps * 32, 2)
-swa_decode_q8_kernel(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ kc,
-                     const uint8_t *__restrict__ vc, const float *__restrict__ k_scale,
+__global__ void __launch_bounds__(kQ8Warps * 32, 4)
+swa_decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const __nv_bfloat16 *__restrict__ q, const float *__restrict__ k_scale,
                      const float *__restrict__ v_scale, const int32_t *__restrict__ pos,
                      __nv_bfloat16 *__restrict__ out, float2 *__restrict__ ws_ml, float *__restrict__ ws_o, int Hkv,
                      int W, int nsplit_max, float scale_log2, int split_len, int kv_rep, int block_log2, int nblk) {
     constexpr bool CLUSTER = MODE == kDecodeWindowCluster;
     using Cfg = DecodeQ8Cfg<D, G>;
     constexpr int CH = Cfg::CH;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
 
     const int split = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
     const int Hq = Hkv * G;
@@ -340,8 +367,8 @@ swa_decode_q8_kernel(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restr
         return;
     }
     const int L = (p >= W - 1) ? W : p + 1;
-    constexpr int kClusterKeys = kDecodeClusterSplits * kDecodeBlk;
-    const int split_keys = CLUSTER ? (L + kClusterKeys - 1) / kClusterKeys * kDecodeBlk : split_len;
+    constexpr int kClusterKeys = kDecodeClusterSplits * kQ8Stage;
+    const int split_keys = CLUSTER ? (L + kClusterKeys - 1) / kClusterKeys * kQ8Stage : split_len;
     if (!CLUSTER && (long long)split * split_keys >= L) return;
     const int begin = (int)min((long long)split * split_keys, (long long)L);
     const int end = min(L, begin + split_keys);
@@ -351,196 +378,257 @@ swa_decode_q8_kernel(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restr
     const int hr = lane >> 2, t4 = lane & 3;
     const bool head_ok = hr < G;
     const uint32_t ring = smem_addr(smem) + warp * Cfg::WARP_RING;
+    const uint32_t bars = smem_addr(smem) + Cfg::OFF_BAR + warp * Cfg::STAGES * 8;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Cfg::OFF_ABORT);
+    const unsigned long long limit = g_wait_limit_ns;
 
     const int Hkv_mem = Hkv / kv_rep, gk = g / kv_rep;
-    const size_t row_stride = (size_t)Hkv_mem * D;
-    const uint8_t *kbase = kc + ((size_t)b * W * Hkv_mem + gk) * D;
-    const uint8_t *vbase = vc + ((size_t)b * W * Hkv_mem + gk) * D;
     const float *ksb = k_scale + (size_t)b * nblk * Hkv_mem + gk;
     const float *vsb = v_scale + (size_t)b * nblk * Hkv_mem + gk;
 
-    const int nblk16 = (end - begin + kDecodeBlk - 1) / kDecodeBlk;
-    const int my_blocks = (nblk16 > warp) ? (nblk16 - warp + kDecodeWarps - 1) / kDecodeWarps : 0;
+    const int nst = (end - begin + kQ8Stage - 1) / kQ8Stage;      // stages of the split; this warp's:
+    const int mine = (nst > warp) ? (nst - warp + kQ8Warps - 1) / kQ8Warps : 0;
 
-    auto issue = [&](int i_local, int stage) {
-        const int blk = warp + i_local * kDecodeWarps;
-        const uint32_t st = ring + stage * Cfg::STAGE_BYTES;
-#pragma unroll
-        for (int c = 0; c < Cfg::CPL; ++c) {
-            const int id = c * 32 + lane;
-            const int r = id / CH, ch = id % CH;
-            const int key = min(begin + blk * kDecodeBlk + r, end - 1);     // clamp: always in bounds
-            if (!in_bounds(key, W)) continue;
-            const uint32_t off = q8_off<D>(r, ch);
-            const size_t rowi = (size_t)key * row_stride + ch * 16;
-            cp_async16(st + off, kbase + rowi);
-            cp_async16(st + Cfg::BLK_BYTES + off, vbase + rowi);
-        }
+    // lane 0: the next of this warp's stages into ring slot `slot`
+    int issue_key = begin + warp * kQ8Stage;
+    auto issue = [&](int slot) {
+        const uint32_t st = ring + slot * Cfg::STAGE_BYTES, bar = bars + slot * 8;
+        mbar_arrive_expect_tx(bar, Cfg::STAGE_BYTES);
+        const int k0 = checked_coord(issue_key, W);               // rows past W arrive as zeros
+        tma_load_4d(st, &tm_k, bar, 0, gk, k0, b);
+        tma_load_4d(st + Cfg::TILE_BYTES, &tm_v, bar, 0, gk, k0, b);
+        issue_key += kQ8Warps * kQ8Stage;
     };
-#pragma unroll
-    for (int s = 0; s < Cfg::STAGES - 1; ++s) {
-        if (s < my_blocks) issue(s, s);
-        cp_async_commit();
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        for (int s = 0; s < kQ8Warps * Cfg::STAGES; ++s) mbar_init(smem_addr(smem) + Cfg::OFF_BAR + 8 * s, 1);
+        mbar_init_fence();
     }
+    __syncthreads();
+    if (lane == 0)
+        for (int i = 0; i < Cfg::STAGES && i < mine; ++i) issue(i);
+    __syncwarp();
 
-    // q of head hr scaled by 2^-x into f16; fragment j of the products takes
-    // d = (4c + t4) * 16 + 4w + {0, 1 | 2, 3}, j = 4c + w
-    uint32_t qa[Cfg::KSTEPS][2];
+    // q of head hr times 2^-x as hi + lo / 16: k-step j = 2c + n takes d = (4c +
+    // t4) * 16 + 8n + {0..3 | 4..7}
+    uint32_t qa[Cfg::KSTEPS][4];
     float qfac;                                     // scale log2(e) 2^x
     {
         const __nv_bfloat16 *qp = q + ((size_t)b * Hq + g * G + (head_ok ? hr : 0)) * D;
-        uint32_t raw[Cfg::KSTEPS][2];
+        uint32_t raw[Cfg::KSTEPS][4];
         uint32_t top = 0;
 #pragma unroll
         for (int j = 0; j < Cfg::KSTEPS; ++j)
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int d = (4 * (j >> 2) + t4) * 16 + 4 * (j & 3) + 2 * hf;
-                raw[j][hf] = head_ok ? __ldg(reinterpret_cast<const uint32_t *>(qp + d)) : 0u;
-                const uint32_t lo = raw[j][hf] & 0x7FFFu, hi = (raw[j][hf] >> 16) & 0x7FFFu;
+            for (int w = 0; w < 4; ++w) {
+                const int d = (4 * (j >> 1) + t4) * 16 + 8 * (j & 1) + 2 * w;
+                raw[j][w] = head_ok ? __ldg(reinterpret_cast<const uint32_t *>(qp + d)) : 0u;
+                const uint32_t lo = raw[j][w] & 0x7FFFu, hi = (raw[j][w] >> 16) & 0x7FFFu;
                 top = max(top, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
             }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // exponent field of the largest |q| (at least 15: below that q is 0 to
-        // any key that fits), brought to that of 2^14
-        const int ef = max(15, (int)(top >> 7));
-        const float down = __uint_as_float((uint32_t)(268 - ef) << 23);
-        qfac = scale_log2 * __uint_as_float((uint32_t)(ef - 14) << 23);
+        // exponent field of the largest |q| (at least 8: below that q is 0 to any
+        // key that fits), brought to that of 2^7
+        const int ef = max(8, (int)(top >> 7));
+        const float down = __uint_as_float((uint32_t)(261 - ef) << 23);
+        qfac = scale_log2 * __uint_as_float((uint32_t)(ef - 7) << 23);
 #pragma unroll
         for (int j = 0; j < Cfg::KSTEPS; ++j)
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-                qa[j][hf] = pack_f16x2(__uint_as_float(raw[j][hf] << 16) * down,
-                                       __uint_as_float(raw[j][hf] & 0xFFFF0000u) * down);
+            for (int hf = 0; hf < 2; ++hf) {
+                uint32_t hi = 0, lo = 0;
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const uint32_t x = raw[j][2 * hf + w];
+                    // not finite: NaN, as neither part could say so otherwise
+                    const float2 y = make_float2(q8_scaled(__uint_as_float(x << 16), down),
+                                                 q8_scaled(__uint_as_float(x & 0xFFFF0000u), down));
+                    const uint32_t c = f32x2_to_e4m3x2(y.x, y.y);
+                    const float2 r = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)c));
+                    hi |= c << (16 * w);
+                    lo |= f32x2_to_e4m3x2((y.x - r.x) * 16.f, (y.y - r.y) * 16.f) << (16 * w);
+                }
+                qa[j][2 * hf] = hi;
+                qa[j][2 * hf + 1] = lo;
+            }
     }
 
-    float m_run = -INFINITY, l_run = 0.f;
-    float o[Cfg::NB][2];
+    float m_run = -INFINITY, l_run = 0.f;           // of head hr, this lane's keys
+    // O^T: rows d = hr * MT * 2 + 2 mt (o[mt][0], [1]) and + 1 ([2], [3]), heads 2 t4 + {0, 1}
+    float2 o[Cfg::MT][2];
 #pragma unroll
-    for (int nb = 0; nb < Cfg::NB; ++nb) o[nb][0] = o[nb][1] = 0.f;
+    for (int mt = 0; mt < Cfg::MT; ++mt) o[mt][0] = o[mt][1] = make_float2(0.f, 0.f);
 
-    // scales of the current block, loaded one block ahead
-    float ks_next = 0.f, vs_next = 0.f;
-    auto load_scales = [&](int i_local) {
-        const int key0 = begin + (warp + i_local * kDecodeWarps) * kDecodeBlk;
-        const size_t si = (size_t)(key0 >> block_log2) * Hkv_mem;
-        if (!in_bounds(key0 >> block_log2, nblk)) return;
-        ks_next = __ldg(ksb + si);
-        vs_next = __ldg(vsb + si);
-    };
-    if (my_blocks > 0) load_scales(0);
-
-    for (int i = 0; i < my_blocks; ++i) {
-        const int stage = i % Cfg::STAGES;
-        cp_async_wait<Cfg::STAGES - 2>();
-        __syncwarp();
-        const float kf = ks_next * qfac, vs = vs_next;
-        {
-            const int nxt = i + Cfg::STAGES - 1;
-            if (nxt < my_blocks) issue(nxt, nxt % Cfg::STAGES);
-            cp_async_commit();
+    // byte offsets of this lane's fragments in a stage: K rows hr (+ 8), V rows
+    // 2 t4 + {0, 1, 8, 9}; 16 rows further on the swizzle repeats
+    uint32_t koff[2][CH / 4], voff[4];
+#pragma unroll
+    for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+        for (int c = 0; c < CH / 4; ++c) koff[nb][c] = ring + q8_off<D>(nb * 8 + hr, c * 4 + t4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int r = 2 * t4 + (e & 1) + (e >> 1) * 8;
+        voff[e] = ring + Cfg::TILE_BYTES + (D == 128 ? q8_off<D>(r, hr) : q8_off<D>(r, hr >> 1) + (hr & 1) * 8);
+    }
+    constexpr int HALVES = kQ8Stage / 16;
+    float ks[HALVES], vs[HALVES];
+    // one scale per 16 keys, loaded a stage ahead of its use
+    auto load_scales = [&](int stage0) {
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h) {
+            const int blk = min(stage0 + 16 * h, end - 1) >> block_log2;
+            if (!in_bounds(blk, nblk)) continue;
+            ks[h] = __ldg(ksb + (size_t)blk * Hkv_mem);
+            vs[h] = __ldg(vsb + (size_t)blk * Hkv_mem);
         }
-        if (i + 1 < my_blocks) load_scales(i + 1);
-        const uint32_t sk = ring + stage * Cfg::STAGE_BYTES, sv = sk + Cfg::BLK_BYTES;
-        const int key0 = begin + (warp + i * kDecodeWarps) * kDecodeBlk;
-
-        float s[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+    };
+    int stage0 = begin + warp * kQ8Stage;
+    if (mine > 0) load_scales(stage0);
+    uint32_t slot = 0, phase = 0;
+    for (int i = 0; i < mine; ++i) {
+        const uint32_t st = slot * Cfg::STAGE_BYTES;
+        float kf[HALVES];
+        float2 vs2[HALVES];
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb)
+        for (int h = 0; h < HALVES; ++h) {
+            kf[h] = ks[h] * qfac;
+            vs2[h] = make_float2(vs[h], vs[h]);
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(bars + slot * 8, phase, abort_flag, limit))) {
+            // let what this warp started land before the block goes on
+            if (lane == 0)
+                for (int j = i; j < min(mine, i + Cfg::STAGES); ++j)
+                    mbar_drain_bounded(bars + (j % Cfg::STAGES) * 8, (j / Cfg::STAGES) & 1, kDrainLimitNs);
+            __syncwarp();
+            break;
+        }
+        if (i + 1 < mine) load_scales(stage0 + kQ8Warps * kQ8Stage);
 #pragma unroll
-            for (int c = 0; c < CH / 4; ++c) {
-                const uint4 w4 = lds128(sk + q8_off<D>(nb * 8 + hr, c * 4 + t4));
-                const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+        for (int h = 0; h < HALVES; ++h) {
+            const int key0 = stage0 + 16 * h;
+            if (key0 >= end) break;
+            const uint32_t at = st + h * 16 * D;
+            // rows 0..7: q hi, rows 8..15: q lo, of keys 8 nb + 2 t4 + {0, 1}
+            float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                for (int c = 0; c < CH / 4; ++c) {
+                    const uint4 w = lds128(koff[nb][c] + at);
+                    mma_e4m3(s[nb], qa[2 * c], w.x, w.y);
+                    mma_e4m3(s[nb], qa[2 * c + 1], w.z, w.w);
+                }
+            const bool tail = key0 + 16 > end;       // uniform; a branch, not predication, keeps it off the others
+            float sc[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[e] = fmaf(s[e >> 1][2 + (e & 1)], 0.0625f, s[e >> 1][e & 1]) * kf[h];
+            if (tail) {
+                asm volatile("" ::: "memory");
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    mma_rows8_f16(s[nb][0], s[nb][1], qa[4 * c + e][0], qa[4 * c + e][1],
-                                  e4m3x2_to_f16x2((uint16_t)w[e]), e4m3x2_to_f16x2((uint16_t)(w[e] >> 16)));
+                    if (key0 + 2 * t4 + (e & 1) + (e >> 1) * 8 >= end) sc[e] = -INFINITY;
             }
-        float sc[4] = {s[0][0], s[0][1], s[1][0], s[1][1]};
-        float mx = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int key = key0 + 2 * t4 + (e & 1) + (e >> 1) * 8;
-            sc[e] = (key < end) ? sc[e] * kf : -INFINITY;
-            mx = fmaxf(mx, sc[e]);
-        }
-        if (__any_sync(0xffffffffu, head_ok && mx > m_run + 8.0f)) {
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            if (mx > m_run) {                    // uniform across the quad
-                const float alpha = ex2_approx(m_run - mx);
-                l_run *= alpha;
-#pragma unroll
-                for (int nb = 0; nb < Cfg::NB; ++nb) {
-                    o[nb][0] *= alpha;
-                    o[nb][1] *= alpha;
+            float mx = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
+            if (__any_sync(0xffffffffu, head_ok && mx > m_run + 8.0f)) {
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                float alpha = 1.f;
+                if (mx > m_run) {                    // uniform across the quad
+                    alpha = ex2_approx(m_run - mx);
+                    l_run *= alpha;
+                    m_run = mx;
                 }
-                m_run = mx;
+                // O^T has the heads across the lanes of a quad
+                const float2 a2 = make_float2(__shfl_sync(0xffffffffu, alpha, 8 * t4),
+                                              __shfl_sync(0xffffffffu, alpha, 8 * t4 + 4));
+#pragma unroll
+                for (int mt = 0; mt < Cfg::MT; ++mt)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        o[mt][r].x *= a2.x;
+                        o[mt][r].y *= a2.y;
+                    }
+            }
+            const float off = 7.0f - m_run;
+            float pw[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) pw[e] = head_ok ? ex2_approx(sc[e] + off) : 0.f;
+            const uint32_t pb0 = pack_f16x2(pw[0], pw[1]), pb1 = pack_f16x2(pw[2], pw[3]);
+            {
+                const float2 l0 = f16x2_to_f32x2(pb0), l1 = f16x2_to_f32x2(pb1);
+                l_run += (l0.x + l0.y) + (l1.x + l1.y);
+            }
+            // V: this lane's 4 keys (2 t4 + {0, 1, 8, 9}), codes d = hr * 2 MT .. + 2 MT - 1
+            uint32_t vw[4][Cfg::MT / 2];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (D == 128) {
+                    const uint4 w4 = lds128(voff[e] + at);
+                    vw[e][0] = w4.x;
+                    vw[e][1] = w4.y;
+                    vw[e][Cfg::MT / 2 - 2] = w4.z;
+                    vw[e][Cfg::MT / 2 - 1] = w4.w;
+                } else {
+                    const uint2 w2 = lds64(voff[e] + at);
+                    vw[e][0] = w2.x;
+                    vw[e][1] = w2.y;
+                }
+            }
+            if (tail) {
+                // a slot behind the last key may hold anything; its weight of 0 has
+                // to meet a 0
+                asm volatile("" ::: "memory");
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (key0 + 2 * t4 + (e & 1) + (e >> 1) * 8 >= end) {
+#pragma unroll
+                        for (int w = 0; w < Cfg::MT / 2; ++w) vw[e][w] = 0u;
+                    }
+            }
+#pragma unroll
+            for (int mt = 0; mt < Cfg::MT; ++mt) {   // byte columns 2 mt, 2 mt + 1
+                const uint32_t sel = (mt & 1) ? 0x7362u : 0x5140u;
+                const uint32_t x = __byte_perm(vw[0][mt >> 1], vw[1][mt >> 1], sel);
+                const uint32_t y = __byte_perm(vw[2][mt >> 1], vw[3][mt >> 1], sel);
+                float t[4];
+                mma_f16(t, e4m3x2_to_f16x2((uint16_t)x), e4m3x2_to_f16x2((uint16_t)(x >> 16)),
+                        e4m3x2_to_f16x2((uint16_t)y), e4m3x2_to_f16x2((uint16_t)(y >> 16)), pb0, pb1);
+                o[mt][0] = ffma2(vs2[h], make_float2(t[0], t[1]), o[mt][0]);
+                o[mt][1] = ffma2(vs2[h], make_float2(t[2], t[3]), o[mt][1]);
             }
         }
-        float pw[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) pw[e] = head_ok ? ex2_approx(sc[e] - m_run + 7.0f) : 0.f;
-        const uint32_t pa0 = pack_f16x2(pw[0], pw[1]), pa2 = pack_f16x2(pw[2], pw[3]);
-        {
-            const float2 l0 = f16x2_to_f32x2(pa0), l1 = f16x2_to_f32x2(pa2);
-            l_run += (l0.x + l0.y) + (l1.x + l1.y);
+        __syncwarp();                                // every lane has read the stage
+        if (lane == 0 && i + Cfg::STAGES < mine) issue(slot);
+        stage0 += kQ8Warps * kQ8Stage;
+        if (++slot == Cfg::STAGES) {
+            slot = 0;
+            phase ^= 1;
         }
-        // V: this lane's 4 keys (2 t4 + {0, 1, 8, 9}), codes hr * NB .. + NB-1
-        uint32_t vw[4][Cfg::NB / 4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int r = 2 * t4 + (e & 1) + (e >> 1) * 8;
-            if (D == 128) {
-                const uint4 w4 = lds128(sv + q8_off<D>(r, hr));
-                vw[e][0] = w4.x;
-                vw[e][1] = w4.y;
-                vw[e][Cfg::NB / 4 - 2] = w4.z;
-                vw[e][Cfg::NB / 4 - 1] = w4.w;
-            } else {
-                const uint2 w2 = lds64(sv + q8_off<D>(r, hr >> 1) + (hr & 1) * 8);
-                vw[e][0] = w2.x;
-                vw[e][1] = w2.y;
-            }
-        }
-#pragma unroll
-        for (int w = 0; w < Cfg::NB / 4; ++w)
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {     // byte columns 4w + 2hf, + 1
-                const uint32_t sel = hf ? 0x7362u : 0x5140u;
-                const uint32_t x = __byte_perm(vw[0][w], vw[1][w], sel), y = __byte_perm(vw[2][w], vw[3][w], sel);
-                const int nb = 4 * w + 2 * hf;
-                float t0 = 0.f, t1 = 0.f, u0 = 0.f, u1 = 0.f;
-                mma_rows8_f16(t0, t1, pa0, pa2, e4m3x2_to_f16x2((uint16_t)x), e4m3x2_to_f16x2((uint16_t)y));
-                mma_rows8_f16(u0, u1, pa0, pa2, e4m3x2_to_f16x2((uint16_t)(x >> 16)),
-                              e4m3x2_to_f16x2((uint16_t)(y >> 16)));
-                o[nb][0] = fmaf(vs, t0, o[nb][0]);
-                o[nb][1] = fmaf(vs, t1, o[nb][1]);
-                o[nb + 1][0] = fmaf(vs, u0, o[nb + 1][0]);
-                o[nb + 1][1] = fmaf(vs, u1, o[nb + 1][1]);
-            }
-        __syncwarp();
     }
-    cp_async_wait<0>();
     l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
     l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
 
     __syncthreads();
     float *mg = reinterpret_cast<float *>(smem);    // [warp][G][D+2]
-    if (head_ok) {
-        float *dst = mg + (warp * G + hr) * (D + 2);
 #pragma unroll
-        for (int nb = 0; nb < Cfg::NB; ++nb) {      // column n of byte nb is d = n * NB + nb
-            dst[(2 * t4) * Cfg::NB + nb] = o[nb][0];
-            dst[(2 * t4 + 1) * Cfg::NB + nb] = o[nb][1];
-        }
-        if (t4 == 0) {
-            dst[D] = m_run;
-            dst[D + 1] = l_run;
+    for (int hh = 0; hh < 2; ++hh) {
+        const int h = 2 * t4 + hh;
+        if (h >= G) break;
+        float *dst = mg + (warp * G + h) * (D + 2) + hr * 2 * Cfg::MT;
+#pragma unroll
+        for (int mt = 0; mt < Cfg::MT; ++mt) {
+            dst[2 * mt] = hh ? o[mt][0].y : o[mt][0].x;
+            dst[2 * mt + 1] = hh ? o[mt][1].y : o[mt][1].x;
         }
     }
-    decode_merge<D, G, CLUSTER>(mg, b, b, (long long)gridDim.z, g, Hkv, split, nsplit, nsplit_max, out, ws_ml, ws_o);
+    if (head_ok && t4 == 0) {
+        mg[(warp * G + hr) * (D + 2) + D] = m_run;
+        mg[(warp * G + hr) * (D + 2) + D + 1] = l_run;
+    }
+    decode_merge<D, G, CLUSTER, kQ8Warps>(mg, b, b, (long long)gridDim.z, g, Hkv, split, nsplit, nsplit_max, out, ws_ml,
+                                          ws_o);
 }
 
 }  // namespace swa

@@ -76,6 +76,28 @@ swa_status_t make_operand_map(CUtensorMap *map, const void *base, uint64_t d0, u
     return SWA_OK;
 }
 
+// 8-bit tensor [d3, d2, d1, d0] (d0 = 64 or 128, innermost, contiguous) as a 4-D
+// TMA map with a (d0, 1, rows, 1) box: `rows` consecutive rows of one head, in
+// the swizzle of their width.  Out-of-range rows read as zero.
+swa_status_t make_codes_map(CUtensorMap *map, const void *base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t d3,
+                            uint32_t rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return cuda_fail(cudaErrorNotSupported);
+    const cuuint64_t dims[4] = {d0, d1, d2, d3};
+    const cuuint64_t strides[3] = {d0, d0 * d1, d0 * d1 * d2};               // bytes, dims 1..3
+    const cuuint32_t box[4] = {(cuuint32_t)d0, 1, rows, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    d0 == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        t_last_cuda_error = static_cast<int>(r);
+        return SWA_ERR_CUDA;
+    }
+    return SWA_OK;
+}
+
 // ----------------------------------------------------------------- device info
 constexpr int kMaxDevices = 64;
 
@@ -104,8 +126,8 @@ swa_status_t device_info(DeviceInfo **out) {
     SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_prefill_weights_kernel<DD, PP>,               \
                                       cudaFuncAttributeMaxDynamicSharedMemorySize,           \
                                       swa::WeightsCfg<DD, PP>::SMEM_ALLOC));
-        SWA_SET_WEIGHTS_ATTR(64, 1) SWA_SET_WEIGHTS_ATTR(64, 2)
-        SWA_SET_WEIGHTS_ATTR(128, 1) SWA_SET_WEIGHTS_ATTR(128, 2)
+        SWA_SET_WEIGHTS_ATTR(64, 1) SWA_SET_WEIGHTS_ATTR(64, 2) SWA_SET_WEIGHTS_ATTR(64, 3)
+        SWA_SET_WEIGHTS_ATTR(128, 1) SWA_SET_WEIGHTS_ATTR(128, 2) SWA_SET_WEIGHTS_ATTR(128, 3)
 #undef SWA_SET_WEIGHTS_ATTR
 #define SWA_SET_DECODE_ATTR(DD, GG)                                                           \
     SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_decode_kernel<DD, GG, swa::kDecodeWindow>,    \
@@ -655,9 +677,12 @@ swa_status_t launch_decode_q8_dg(const void *q, const void *kc, const void *vc, 
     int block_log2 = 0;
     while ((1 << block_log2) < block) ++block_log2;
     const int nblk = (int)(((long long)W + block - 1) / block);
+    CUtensorMap mk, mv;
+    if (swa_status_t e = make_codes_map(&mk, kc, D, Hkv / kv_rep, W, B, swa::kQ8Stage)) return e;
+    if (swa_status_t e = make_codes_map(&mv, vc, D, Hkv / kv_rep, W, B, swa::kQ8Stage)) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(nsm, Hkv, B);
-    cfg.blockDim = dim3(swa::kDecodeWarps * 32);
+    cfg.blockDim = dim3(swa::kQ8Warps * 32);
     cfg.dynamicSmemBytes = swa::DecodeQ8Cfg<D, G>::SMEM_BYTES;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -669,8 +694,7 @@ swa_status_t launch_decode_q8_dg(const void *q, const void *kc, const void *vc, 
     cfg.numAttrs = cluster ? 1 : 0;
     auto kernel = cluster ? swa::swa_decode_q8_kernel<D, G, swa::kDecodeWindowCluster>
                           : swa::swa_decode_q8_kernel<D, G, swa::kDecodeWindow>;
-    SWA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, static_cast<const __nv_bfloat16 *>(q),
-                                    static_cast<const uint8_t *>(kc), static_cast<const uint8_t *>(vc), ks, vs, pos,
+    SWA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, mk, mv, static_cast<const __nv_bfloat16 *>(q), ks, vs, pos,
                                     static_cast<__nv_bfloat16 *>(out), ws_ml, ws_o, Hkv, W, nsm, scale * kLog2e,
                                     split, kv_rep, block_log2, nblk));
     if (nsm > 1 && !cluster) {
@@ -880,22 +904,25 @@ swa_status_t keep_impl(const void *k, const void *v, const float *weights, const
 }
 
 // ----------------------------------------------------------------- weights of a prompt
-// Sizes and workspace of swa_prefill_weights: pass 1's partial results, lse,
-// pass 2's partial results.  The streamed tiles of a unit are split when the
-// units alone would not give kWeightsUnits (two for each SM), down to 4 tiles.
-// A function of the sizes only, as the workspace size is.
+// Sizes and workspace of swa_prefill_weights: the lse pass's partial results,
+// lse, the weights pass's partial planes.  A function of the sizes only, as the
+// workspace size is.
 struct WeightsLayout {
-    int G, TQ, nqt, nkt, splits1, splits2;
+    int G, TQ, nqt, nkt, splits1, splits2, planes;
+    bool by_query;               // all queries fit in two tiles: they stay in the weights pass too
     long long units1, units2;
     size_t lse_off, part_off, bytes;
 };
 
-constexpr long long kWeightsUnits = 296;
+constexpr int kWeightsBlocks = 148;              // persistent blocks the splits aim at: one per SM
 
-int weights_splits(long long units, long long tiles) {
-    long long want = (kWeightsUnits + units - 1) / units;
-    if (want > tiles / 4) want = tiles / 4;
-    return (int)(want < 1 ? 1 : want > 64 ? 64 : want);
+// Splits of a unit's `tiles` streamed tiles.  Units of about the same work fill
+// one wave of the persistent blocks; where the work falls off along a triangle,
+// six units to a block keep the last ones short.  At least `least` tiles each.
+int weights_splits(long long units, long long tiles, bool even, int least) {
+    long long s = even ? kWeightsBlocks / units : (6 * kWeightsBlocks + units - 1) / units;
+    if (s > tiles / least) s = tiles / least;
+    return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
 
 WeightsLayout weights_layout(int B, int T, int N, int Hq, int Hkv, int W) {
@@ -904,17 +931,21 @@ WeightsLayout weights_layout(int B, int T, int N, int Hq, int Hkv, int W) {
     l.TQ = 128 / l.G;
     l.nqt = (int)(((long long)T + l.TQ - 1) / l.TQ);
     l.nkt = (int)(((long long)N + 127) / 128);
+    l.by_query = l.nqt <= 2;
     const long long weff = W < N ? W : N;
-    const long long t1 = (weff + l.TQ - 2) / 128 + 2, t2 = (weff + 126) / l.TQ + 2;
+    const long long t1 = (weff + 2 * l.TQ - 2) / 128 + 2, t2 = (weff + 254) / l.TQ + 2;
     const long long bh = (long long)B * Hkv;
-    l.splits1 = weights_splits(bh * l.nqt, t1 < l.nkt ? t1 : l.nkt);
-    l.splits2 = weights_splits(bh * l.nkt, t2 < l.nqt ? t2 : l.nqt);
-    l.units1 = bh * l.nqt * l.splits1;
-    l.units2 = bh * l.nkt * l.splits2;
+    const bool even = T <= N / 4 || W <= N / 4;
+    const long long pairs1 = (l.nqt + 1) / 2, pairs2 = (l.nkt + 1) / 2;
+    l.splits1 = weights_splits(bh * pairs1, t1 < l.nkt ? t1 : l.nkt, even, 2);
+    l.splits2 = l.by_query ? l.splits1 : weights_splits(bh * pairs2, t2 < l.nqt ? t2 : l.nqt, even, 4);
+    l.units1 = bh * pairs1 * l.splits1;
+    l.units2 = l.by_query ? bh * l.splits2 : bh * pairs2 * l.splits2;
+    l.planes = 2 * (l.by_query ? l.nqt : l.splits2);
     const size_t rows = (size_t)bh * l.nqt * 128;
     l.lse_off = rows * 2 * l.splits1 * 8;
     l.part_off = (l.lse_off + rows * 4 + 255) & ~size_t(255);
-    l.bytes = l.part_off + (size_t)2 * l.splits2 * bh * N * 4;
+    l.bytes = l.part_off + (size_t)l.planes * bh * N * 4;
     return l;
 }
 
@@ -927,14 +958,26 @@ swa_status_t prefill_weights_sizes(int B, int T, int N, int Hq, int Hkv, int D, 
     return SWA_OK;
 }
 
-template <int D, int PASS>
+template <int D, int MODE>
 swa_status_t launch_weights_pass(const CUtensorMap &mq, const CUtensorMap &mk, const swa::WeightsParams &p, int sms,
                                  cudaStream_t s) {
     const int grid = p.num_units < sms ? p.num_units : sms;
-    swa::swa_prefill_weights_kernel<D, PASS>
-        <<<grid, swa::WeightsCfg<D, PASS>::THREADS, swa::WeightsCfg<D, PASS>::SMEM_ALLOC, s>>>(mq, mk, p);
+    swa::swa_prefill_weights_kernel<D, MODE>
+        <<<grid, swa::WeightsCfg<D, MODE>::THREADS, swa::WeightsCfg<D, MODE>::SMEM_ALLOC, s>>>(mq, mk, p);
     SWA_CUDA_TRY(cudaGetLastError());
     return SWA_OK;
+}
+
+swa_status_t launch_weights_pass(int mode, int D, const CUtensorMap &mq, const CUtensorMap &mk,
+                                 const swa::WeightsParams &p, int sms, cudaStream_t s) {
+    switch (mode + (D == 128 ? 4 : 0)) {
+        case swa::kWeightsLse: return launch_weights_pass<64, swa::kWeightsLse>(mq, mk, p, sms, s);
+        case swa::kWeightsByKey: return launch_weights_pass<64, swa::kWeightsByKey>(mq, mk, p, sms, s);
+        case swa::kWeightsByQuery: return launch_weights_pass<64, swa::kWeightsByQuery>(mq, mk, p, sms, s);
+        case swa::kWeightsLse + 4: return launch_weights_pass<128, swa::kWeightsLse>(mq, mk, p, sms, s);
+        case swa::kWeightsByKey + 4: return launch_weights_pass<128, swa::kWeightsByKey>(mq, mk, p, sms, s);
+        default: return launch_weights_pass<128, swa::kWeightsByQuery>(mq, mk, p, sms, s);
+    }
 }
 
 swa_status_t prefill_weights_impl(const void *q, const void *k, const int32_t *lens, float *weights, int B, int T,
@@ -964,21 +1007,19 @@ swa_status_t prefill_weights_impl(const void *q, const void *k, const int32_t *l
     p.part = part;
     p.splits = l.splits1;
     p.num_units = (int)l.units1;
-    if (swa_status_t e = D == 128 ? launch_weights_pass<128, 1>(mq, mk, p, dev->sms, s)
-                                  : launch_weights_pass<64, 1>(mq, mk, p, dev->sms, s))
-        return e;
+    if (swa_status_t e = launch_weights_pass(swa::kWeightsLse, D, mq, mk, p, dev->sms, s)) return e;
     swa::swa_weights_lse_kernel<<<(unsigned)((long long)B * Hkv * l.nqt), 128, 0, s>>>(
         p.ml, lse, lens, N, T, Hkv, l.G, l.TQ, l.nqt, 2 * l.splits1);
     SWA_CUDA_TRY(cudaGetLastError());
     p.splits = l.splits2;
     p.num_units = (int)l.units2;
-    if (swa_status_t e = D == 128 ? launch_weights_pass<128, 2>(mq, mk, p, dev->sms, s)
-                                  : launch_weights_pass<64, 2>(mq, mk, p, dev->sms, s))
+    if (swa_status_t e = launch_weights_pass(l.by_query ? swa::kWeightsByQuery : swa::kWeightsByKey, D, mq, mk, p,
+                                             dev->sms, s))
         return e;
     const long long n = (long long)B * Hkv * N;
     long long blocks = (n + 255) / 256;
     if (blocks > (long long)dev->sms * 16) blocks = (long long)dev->sms * 16;
-    swa::swa_weights_sum_kernel<<<(int)blocks, 256, 0, s>>>(part, weights, n, 2 * l.splits2);
+    swa::swa_weights_sum_kernel<<<(int)blocks, 256, 0, s>>>(p, weights, l.planes, l.by_query);
     SWA_CUDA_TRY(cudaGetLastError());
     return SWA_OK;
 }

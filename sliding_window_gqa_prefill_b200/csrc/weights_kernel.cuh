@@ -6,44 +6,50 @@
 //
 // The sum over queries needs lse, which needs every key of the window first, so
 // there are two passes over Q K^T, each a persistent tcgen05 kernel of one
-// shape: a stationary 128-row tile A in shared memory, tiles B streamed through
-// a ring by TMA, D = A B^T in tensor memory, and one thread per row of A that
-// reduces along its row, so that no reduction crosses threads:
-//  * pass 1 (lse): A = 128 (query, head) rows of one KV head's group, B = key
-//    tiles; a row keeps a running maximum and sum;
-//  * pass 2 (weights): A = 128 keys, B = tiles of (query, head) rows; a row (a
-//    key) adds 2^(x - lse), lse coming along with the tile.  Each key is owned
-//    by one thread: no atomics, and the order of the sum is fixed.
+// shape: up to two 128-row tiles stay in shared memory, tiles of the other
+// operand are streamed past them through a ring by TMA, the products go to
+// tensor memory, and one thread per row of a product reduces along its row, so
+// that no reduction crosses threads and no score is ever written:
+//  * lse: rows are queries; a row keeps a running maximum and sum;
+//  * weights: rows are keys; a row adds 2^(x - lse), lse coming along with the
+//    queries.  Each key is owned by one thread: no atomics, and the order of
+//    the sum is fixed.  Either two key tiles stay and the queries are streamed,
+//    or, when all queries fit in two tiles, they stay and the keys are streamed.
 // A tile of queries holds TQ = floor(128 / G) positions times the G heads of
-// the group (position-major), one TMA box.  Neither pass writes the scores.
+// the group (position-major), one TMA box.
 //
-// Warps: 0 TMA, 1 MMA (one thread each), 2 tensor-memory allocation, 4-7 and
-// 8-11 the two reducing warpgroups, which take the tiles of a unit in turn.
-// Tensor memory holds four 128 x 128 fp32 results, so the tensor core runs up
-// to four tiles ahead of the reduction.  Each warpgroup leaves its own partial
-// result; small kernels join them.
+// Warps: 0 TMA, 1 MMA (one thread each), 2 tensor-memory allocation, 4-19 the
+// four reducing warpgroups.  Warpgroup w reduces columns 64 (w >> 1) .. + 63 of
+// the products of stationary tile w & 1.  Tensor memory holds two 128 x 128 fp32
+// products of each stationary tile; a warpgroup reads its 64 columns in two
+// loads and gives the product back halfway through, so the tensor core is up to
+// a step and a half ahead.  (One product per warpgroup, given back at three
+// quarters, left it waiting: both measured 690 to 700 us at T = N = 8192, 32 / 8 heads.)
+//
+// What bounds it: one exponential per score and pass, 16 per clock and SM on
+// the special-function unit: 1024 clocks for a 128 x 128 product whose MMA takes
+// 512.  kWeightsPoly pairs in 16 therefore go to a polynomial on the FMA pipe.
 #pragma once
 
 #include "weights_plan.cuh"
 
 namespace swa {
 
-template <int D, int PASS>
+template <int D, int MODE>
 struct WeightsCfg {
     static constexpr int NREG = D / 64;
     static constexpr int REGION_BYTES = 128 * 128;
     static constexpr int TILE_BYTES = NREG * REGION_BYTES;
     static constexpr int STAGES = 4;
-    static constexpr int BUFS = 4;                       // results in tensor memory
-    static constexpr int OFF_A = 0;
-    static constexpr int OFF_B = TILE_BYTES;
-    static constexpr int OFF_LSE = OFF_B + STAGES * TILE_BYTES;          // [STAGES][128] floats
+    static constexpr int OFF_A = 0;                                      // two stationary tiles
+    static constexpr int OFF_B = 2 * TILE_BYTES;
+    static constexpr int OFF_LSE = OFF_B + STAGES * TILE_BYTES;          // 128 floats per stage / stationary tile
     static constexpr int OFF_BAR = OFF_LSE + STAGES * 512;
-    // a_full, a_empty, b_full[STAGES], b_empty[STAGES], s_full[BUFS], s_empty[BUFS], drain
-    static constexpr int NBAR = 2 + 2 * STAGES + 2 * BUFS + 1;
+    // a_full, a_empty, b_full[STAGES], b_empty[STAGES], s_full[4], s_empty[4], drain
+    static constexpr int NBAR = 2 + 2 * STAGES + 8 + 1;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM_ALLOC = OFF_MISC + 16 + 1024;              // slack for 1024-byte alignment
-    static constexpr int THREADS = 384;
+    static constexpr int THREADS = 640;
     static constexpr uint32_t IDESC = make_idesc_bf16(128, 128, 0);
     static_assert(D == 64 || D == 128, "head_dim 64 or 128");
     static_assert(SMEM_ALLOC <= 232448, "dynamic shared memory of one block (227 KB)");
@@ -57,12 +63,53 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
-template <int D, int PASS>
-__global__ void __launch_bounds__(384, 1)
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+
+// The largest of three, NaN ignored as by fmaxf.
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+__device__ __forceinline__ float4 lds_f32x4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+    return v;
+}
+
+// 2^x for two values on the FMA pipe, as exp2_poly2 but to the accuracy of the
+// special-function unit: degree 5, fitted in the same way (relative error
+// 1.3e-7 in fp32).  x is clamped at -126.
+__device__ __forceinline__ float2 exp2_poly2_fine(float2 x) {
+    constexpr float kShift = 12582912.0f;                       // 1.5 * 2^23
+    constexpr float c1 = 0.69314694f, c2 = 0.24022120f, c3 = 0.055507131f, c4 = 0.0096755410f, c5 = 0.0013276471f;
+    x.x = fmaxf(x.x, -126.0f);
+    x.y = fmaxf(x.y, -126.0f);
+    const float2 t = fadd2(x, make_float2(kShift, kShift));
+    const float2 n = fadd2(t, make_float2(-kShift, -kShift));    // round(x), exact
+    const float2 f = ffma2(n, make_float2(-1.0f, -1.0f), x);     // x - n, exact
+    float2 p = ffma2(f, make_float2(c5, c5), make_float2(c4, c4));
+    p = ffma2(p, f, make_float2(c3, c3));
+    p = ffma2(p, f, make_float2(c2, c2));
+    p = ffma2(p, f, make_float2(c1, c1));
+    p = ffma2(p, f, make_float2(1.0f, 1.0f));
+    return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                       __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+}
+
+// which of the 16 column pairs of 32 columns take the polynomial
+constexpr uint32_t kWeightsPoly = 0x1111u;
+
+template <int D, int MODE>
+__global__ void __launch_bounds__(640, 1)
 swa_prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                            const WeightsParams p) {
-    using Cfg = WeightsCfg<D, PASS>;
-    constexpr int NREG = Cfg::NREG, RB = Cfg::REGION_BYTES, TB = Cfg::TILE_BYTES, ST = Cfg::STAGES, NB = Cfg::BUFS;
+    using Cfg = WeightsCfg<D, MODE>;
+    constexpr int NREG = Cfg::NREG, RB = Cfg::REGION_BYTES, TB = Cfg::TILE_BYTES, ST = Cfg::STAGES;
+    constexpr bool Q_STAYS = MODE != kWeightsByKey, ROW_IS_QUERY = MODE == kWeightsLse;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
@@ -70,8 +117,8 @@ swa_prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
     const uint32_t sA = sbase + Cfg::OFF_A, sB = sbase + Cfg::OFF_B;
     const uint32_t bar_a_full = sbase + Cfg::OFF_BAR, bar_a_empty = bar_a_full + 8;
     const uint32_t bar_b_full = bar_a_empty + 8, bar_b_empty = bar_b_full + 8 * ST;
-    const uint32_t bar_s_full = bar_b_empty + 8 * ST, bar_s_empty = bar_s_full + 8 * NB;
-    const uint32_t bar_drain = bar_s_empty + 8 * NB;
+    const uint32_t bar_s_full = bar_b_empty + 8 * ST, bar_s_empty = bar_s_full + 32;
+    const uint32_t bar_drain = bar_s_empty + 32;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Cfg::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Cfg::OFF_MISC + 4);
 
@@ -82,15 +129,18 @@ swa_prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
 
     if (threadIdx.x == 0) {
         mbar_init(bar_a_full, 1);
-        mbar_init(bar_a_empty, 1);
+        // the tensor core, and where lse comes with the stationary queries the
+        // 16 reducing warps, which read it
+        mbar_init(bar_a_empty, MODE == kWeightsByQuery ? 17 : 1);
         for (int s = 0; s < ST; ++s) {
             mbar_init(bar_b_full + 8 * s, 1);
-            // pass 2: the reducing warps read the stage's lse as well
-            mbar_init(bar_b_empty + 8 * s, PASS == 2 ? 5 : 1);
+            // where lse comes with the streamed queries, the 16 warps that reduce
+            // the stage's two products (8, arriving for 16, if there is one)
+            mbar_init(bar_b_empty + 8 * s, MODE == kWeightsByKey ? 17 : 1);
         }
-        for (int s = 0; s < NB; ++s) {
+        for (int s = 0; s < 4; ++s) {
             mbar_init(bar_s_full + 8 * s, 1);
-            mbar_init(bar_s_empty + 8 * s, 4);
+            mbar_init(bar_s_empty + 8 * s, 8);
         }
         mbar_init(bar_drain, 1);
         *abort_flag = 0;
@@ -99,7 +149,7 @@ swa_prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
         prefetch_tensormap(&tm_k);
     }
     // rows of a query tile past TQ * G are never written by TMA: zeros
-    for (int t = PASS == 1 ? 0 : 1; t < (PASS == 1 ? 1 : 1 + ST); ++t)
+    for (int t = Q_STAYS ? 0 : 2; t < (Q_STAYS ? 2 : 2 + ST); ++t)
         for (int r = 0; r < NREG; ++r)
             for (int i = qrows * 8 + threadIdx.x; i < 1024; i += Cfg::THREADS)
                 reinterpret_cast<uint4 *>(smem + t * TB + r * RB)[i] = make_uint4(0, 0, 0, 0);
@@ -112,13 +162,15 @@ swa_prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    auto unit = [&](long long u) {
+        return weights_unit<MODE>(p, (int)u, weights_len(__ldg(p.lens + (int)(u / p.Hkv % p.B)), p.N));
+    };
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
         if (lane == 0) {
             uint32_t bc = 0, uc = 0, b_cnt[ST] = {};
             bool ok = true;
-            // rows of a tile of keys, or of a tile of queries
             auto load_k = [&](uint32_t dst, uint32_t bar, const WeightsUnit &U, int tile) {
                 for (int r = 0; r < NREG; ++r)
                     tma_load_4d(dst + r * RB, &tm_k, bar, r * 64, checked_coord(U.g, p.Hkv),
@@ -129,30 +181,35 @@ swa_prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
                     tma_load_4d(dst + r * RB, &tm_q, bar, r * 64, checked_coord(U.g * p.G, p.Hkv * p.G),
                                 checked_coord(tile * p.TQ, p.T), checked_coord(U.b, p.B));
             };
-            for (int u = blockIdx.x; u < p.num_units && ok; u += gridDim.x) {
-                const int b = u / p.Hkv % p.B;
-                const WeightsUnit U = weights_unit<PASS>(p, u, weights_len(__ldg(p.lens + b), p.N));
+            auto load_lse = [&](int slot, uint32_t bar, const WeightsUnit &U, int tile) {
+                bulk_load(sbase + Cfg::OFF_LSE + slot * 512,
+                          p.lse + (((size_t)U.b * p.Hkv + U.g) * p.nqt + checked_coord(tile, p.nqt)) * 128, 512, bar);
+            };
+            long long u;
+            for (int k = 0; (u = weights_unit_of(k, blockIdx.x, gridDim.x)) < p.num_units && ok; ++k) {
+                const WeightsUnit U = unit(u);
                 if (U.n == 0) continue;
                 if (!mbar_wait_bounded(bar_a_empty, (uc & 1) ^ 1, abort_flag, limit)) { ok = false; break; }
                 ++uc;
-                mbar_arrive_expect_tx(bar_a_full, PASS == 1 ? q_bytes : (uint32_t)TB);
-                if (PASS == 1) load_q(sA, bar_a_full, U, U.a);
-                else load_k(sA, bar_a_full, U, U.a);
+                const uint32_t lse_bytes = MODE == kWeightsByQuery ? 512u : 0u;
+                mbar_arrive_expect_tx(bar_a_full, (1 + U.act1) * ((Q_STAYS ? q_bytes : (uint32_t)TB) + lse_bytes));
+                for (int i = 0; i <= (int)U.act1; ++i) {
+                    if (Q_STAYS) load_q(sA + i * TB, bar_a_full, U, U.a + i);
+                    else load_k(sA + i * TB, bar_a_full, U, U.a + i);
+                    if (MODE == kWeightsByQuery) load_lse(i, bar_a_full, U, U.a + i);
+                }
                 for (int j = 0; j < U.n; ++j, ++bc) {
-                    const uint32_t s = bc % ST;
+                    const uint32_t s = bc % ST, bar = bar_b_full + 8 * s;
                     if (!mbar_wait_bounded(bar_b_empty + 8 * s, ((bc / ST) & 1) ^ 1, abort_flag, limit)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t bar = bar_b_full + 8 * s;
-                    mbar_arrive_expect_tx(bar, PASS == 1 ? (uint32_t)TB : q_bytes + 512u);
-                    if (PASS == 1) {
+                    mbar_arrive_expect_tx(bar, Q_STAYS ? (uint32_t)TB : q_bytes + 512u);
+                    if (Q_STAYS) {
                         load_k(sB + s * TB, bar, U, U.first + j);
                     } else {
                         load_q(sB + s * TB, bar, U, U.first + j);
-                        const int qt = checked_coord(U.first + j, p.nqt);
-                        bulk_load(sbase + Cfg::OFF_LSE + s * 512,
-                                  p.lse + ((((size_t)U.b * p.Hkv + U.g) * p.nqt) + qt) * 128, 512, bar);
+                        load_lse(s, bar, U, U.first + j);
                     }
                     ++b_cnt[s];
                 }
@@ -169,29 +226,39 @@ swa_prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
         if (lane == 0) {
             constexpr uint32_t kDescHi = smem_desc_hi(1024);
             const uint32_t adesc = smem_desc_lo(sA, 16), bdesc = smem_desc_lo(sB, 16);
-            uint32_t bc = 0, uc = 0;
+            uint32_t bc = 0, uc = 0, cnt[2] = {0, 0};
             bool ok = true;
-            for (int u = blockIdx.x; u < p.num_units && ok; u += gridDim.x) {
-                const int b = u / p.Hkv % p.B;
-                const WeightsUnit U = weights_unit<PASS>(p, u, weights_len(__ldg(p.lens + b), p.N));
+            long long u;
+            for (int k = 0; (u = weights_unit_of(k, blockIdx.x, gridDim.x)) < p.num_units && ok; ++k) {
+                const WeightsUnit U = unit(u);
                 if (U.n == 0) continue;
                 if (!mbar_wait_bounded(bar_a_full, uc & 1, abort_flag, limit)) { ok = false; break; }
                 ++uc;
-                for (int j = 0; j < U.n; ++j, ++bc) {
-                    const uint32_t s = bc % ST, d = bc % NB;
-                    if (!mbar_wait_bounded(bar_b_full + 8 * s, (bc / ST) & 1, abort_flag, limit) ||
-                        !mbar_wait_bounded(bar_s_empty + 8 * d, ((bc / NB) & 1) ^ 1, abort_flag, limit)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
+                for (int j = 0; j < U.n && ok; ++j, ++bc) {
+                    const uint32_t s = bc % ST;
+                    if (!mbar_wait_bounded(bar_b_full + 8 * s, (bc / ST) & 1, abort_flag, limit)) { ok = false; break; }
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = ((kk >> 2) * RB + (kk & 3) * 32) >> 4;
-                        mma_ss(tmem + d * 128, smem_desc64(adesc + off, kDescHi),
-                               smem_desc64(bdesc + s * (TB >> 4) + off, kDescHi), Cfg::IDESC, kk > 0);
+                    for (int i = 0; i < 2; ++i) {
+                        if (i == 1 && !U.act1) break;
+                        const uint32_t d = i + 2 * (cnt[i] & 1);
+                        if (!mbar_wait_bounded(bar_s_empty + 8 * d, ((cnt[i] >> 1) & 1) ^ 1, abort_flag, limit)) {
+                            ok = false;
+                            break;
+                        }
+                        ++cnt[i];
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = ((kk >> 2) * RB + (kk & 3) * 32) >> 4;
+                            const uint64_t st = smem_desc64(adesc + i * (TB >> 4) + off, kDescHi);
+                            const uint64_t fl = smem_desc64(bdesc + s * (TB >> 4) + off, kDescHi);
+                            // rows: the stationary tile, or the streamed keys
+                            if (MODE == kWeightsByQuery) mma_ss(tmem + d * 128, fl, st, Cfg::IDESC, kk > 0);
+                            else mma_ss(tmem + d * 128, st, fl, Cfg::IDESC, kk > 0);
+                        }
+                        mma_commit(bar_s_full + 8 * d);
                     }
-                    mma_commit(bar_s_full + 8 * d);
+                    if (!ok) break;
                     mma_commit(bar_b_empty + 8 * s);
                     if (j == U.n - 1) mma_commit(bar_a_empty);
                 }
@@ -205,98 +272,130 @@ swa_prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
     } else if (warp >= 4) {
         // ------------------------------------------------------------ reducing warpgroups
         const int wg = (warp - 4) >> 2;
-        const int row = (warp & 3) * 32 + lane;              // row of the stationary tile
-        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-        const float sl2 = p.scale_log2;
-        uint32_t bc0 = 0;
+        const int i = wg & 1, half = wg >> 1;                // stationary tile; columns of its products
+        const int row = (warp & 3) * 32 + lane;              // row of the product
+        const int row_pos = row / p.G;
+        const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + i * 128 + half * 64;
+        const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
+        uint32_t cnt = 0, bc0 = 0, uc = 0;
         bool ok = true;
-        for (int u = blockIdx.x; u < p.num_units && ok; u += gridDim.x) {
-            const int b = u / p.Hkv % p.B;
-            const WeightsUnit U = weights_unit<PASS>(p, u, weights_len(__ldg(p.lens + b), p.N));
-            float m = -INFINITY, l = 0.f;                    // pass 2: l alone
-            for (int j = wg; j < U.n; j += 2) {
-                const uint32_t bc = bc0 + j, d = bc % NB, s = bc % ST;
-                bool got = mbar_wait_bounded(bar_s_full + 8 * d, (bc / NB) & 1, abort_flag, limit);
-                // the tile's lse came by the same barrier as its rows
-                if (PASS == 2 && got) got = mbar_wait_bounded(bar_b_full + 8 * s, (bc / ST) & 1, abort_flag, limit);
+        long long u;
+        for (int k = 0; (u = weights_unit_of(k, blockIdx.x, gridDim.x)) < p.num_units && ok; ++k) {
+            const WeightsUnit U = unit(u);
+            const bool active = i == 0 || U.act1;
+            const size_t bg = (size_t)U.b * p.Hkv + U.g;
+            const WeightsClear clear = weights_clear<Q_STAYS>(p, U, i);
+            float m = -INFINITY, l = 0.f;                    // weights: l alone
+            if (MODE == kWeightsByQuery && U.n > 0) {        // lse came with the stationary queries
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_a_full, uc & 1, abort_flag, limit))) {
+                    ok = false;
+                    break;
+                }
+                ++uc;
+            }
+            for (int j = 0; active && j < U.n; ++j) {
+                const uint32_t s = (bc0 + j) % ST, d = i + 2 * ((cnt + j) & 1);
+                bool got = mbar_wait_bounded(bar_s_full + 8 * d, ((cnt + j) >> 1) & 1, abort_flag, limit);
+                // lse came with the stage's queries
+                if (MODE == kWeightsByKey && got)
+                    got = mbar_wait_bounded(bar_b_full + 8 * s, ((bc0 + j) / ST) & 1, abort_flag, limit);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                uint32_t r[4][32];
+                const int tile = U.first + j;
+                const bool masked = tile < clear.lo || tile > clear.hi;
+                const uint32_t lse_s = sbase + Cfg::OFF_LSE + (MODE == kWeightsByKey ? s : (uint32_t)i) * 512 + half * 256;
+                const uint32_t tD = tS + 256 * ((cnt + j) & 1);
+                uint32_t r[2][32];
+                tmem_ld32(tD, r[0]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(tmem + lane_off + d * 128 + c * 32, r[c]);
-                tmem_wait_ld();
-#pragma unroll
-                for (int c = 0; c < 4; ++c) reg_fence32(r[c]);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_s_empty + 8 * d);
-
-                const WeightsMask M = weights_mask<PASS>(p, U, U.first + j, row);
-                if (M.masked) {
-#pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c < M.lo || c >= M.hi) r[c >> 5][c & 31] = 0xFF800000u;      // -inf
-                }
-                if (PASS == 1) {
-                    float mx[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) mx[e] = __uint_as_float(r[0][e]);
-#pragma unroll
-                    for (int c = 8; c < 128; ++c) mx[c & 7] = fmaxf(mx[c & 7], __uint_as_float(r[c >> 5][c & 31]));
-                    float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                     fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * sl2;
-                    // the offset is raised when the tile exceeds it by more than
-                    // 2^8: the sum keeps its 24 bits either way
-                    if (mt > m + 8.0f) {
-                        l *= ex2_approx(m - mt);
-                        m = mt;
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t(&x)[32] = r[c & 1];
+                    tmem_wait_ld();
+                    reg_fence32(x);
+                    if (c == 0) {
+                        tmem_ld32(tD + 32, r[1]);
+                    } else {                                 // the product is in registers: give it back
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar_s_empty + 8 * d);
                     }
-                }
-                const float off = PASS == 1 ? (m == -INFINITY ? 0.f : m) : 0.f;
-                const float2 sl2x2 = make_float2(sl2, sl2), noff = make_float2(-off, -off);
-                const uint32_t lse_s = sbase + Cfg::OFF_LSE + s * 512;
-                float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                                 make_float2(0.f, 0.f)};
+                    if (masked) {
+                        const WeightsMask M = weights_mask<ROW_IS_QUERY>(p, U, Q_STAYS ? U.a + i : tile,
+                                                                         Q_STAYS ? tile : U.a + i, row, row_pos);
+                        const int lo = M.lo - half * 64 - c * 32, hi = M.hi - half * 64 - c * 32;
 #pragma unroll
-                for (int c = 0; c < 128; c += 4) {
-                    float2 n0 = noff, n1 = noff;
-                    if (PASS == 2) {                         // lse is kept negated
-                        float4 v;
-                        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                                     : "r"(lse_s + c * 4)
-                                     : "memory");
-                        n0 = make_float2(v.x, v.y);
-                        n1 = make_float2(v.z, v.w);
+                        for (int e = 0; e < 32; ++e)
+                            if (e < lo || e >= hi) x[e] = 0xFF800000u;                            // -inf
                     }
-                    const uint32_t *x = &r[c >> 5][c & 31];
-                    const float2 a = ffma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), sl2x2, n0);
-                    const float2 e = ffma2(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), sl2x2, n1);
-                    acc[(c >> 2) & 1] = fadd2(acc[(c >> 2) & 1], make_float2(ex2_approx(a.x), ex2_approx(a.y)));
-                    acc[2 + ((c >> 2) & 1)] = fadd2(acc[2 + ((c >> 2) & 1)], make_float2(ex2_approx(e.x), ex2_approx(e.y)));
+                    float2 off = make_float2(0.f, 0.f);
+                    if (ROW_IS_QUERY) {
+                        float mx[2] = {__uint_as_float(x[0]), __uint_as_float(x[1])};
+#pragma unroll
+                        for (int e = 2; e < 30; e += 4) {
+                            mx[0] = fmax3(mx[0], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                            mx[1] = fmax3(mx[1], __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+                        }
+                        mx[0] = fmax3(mx[0], __uint_as_float(x[30]), __uint_as_float(x[31]));
+                        const float mt = fmaxf(mx[0], mx[1]) * sl2.x;
+                        // the offset is raised when a score exceeds it by more than
+                        // 2^8: the sum keeps its 24 bits either way
+                        if (mt > m + 8.0f) {
+                            l *= ex2_approx(m - mt);
+                            m = mt;
+                        }
+                        off.x = off.y = m == -INFINITY ? 0.f : -m;
+                    }
+                    float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    // 2^-inf of a masked score is to be 0 exactly: not the polynomial
+                    auto add = [&](uint32_t poly) {
+                        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            if (!ROW_IS_QUERY && e % 2 == 0) v = lds_f32x4(lse_s + c * 128 + e * 8);     // -lse
+                            const float2 o = ROW_IS_QUERY ? off : e % 2 ? make_float2(v.z, v.w) : make_float2(v.x, v.y);
+                            const float2 y = ffma2(
+                                make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sl2, o);
+                            acc[e & 1] = fadd2(acc[e & 1], ((poly >> e) & 1u)
+                                                               ? exp2_poly2_fine(y)
+                                                               : make_float2(ex2_approx(y.x), ex2_approx(y.y)));
+                        }
+                    };
+                    if (masked) add(0u);
+                    else add(kWeightsPoly);
+                    const float2 sum = fadd2(acc[0], acc[1]);
+                    l += sum.x + sum.y;
                 }
-                const float2 sum = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
-                l += sum.x + sum.y;
-                if (PASS == 2) {
+                if (MODE == kWeightsByKey) {
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_b_empty + 8 * s);
+                    if (lane == 0) mbar_arrive_n(bar_b_empty + 8 * s, U.act1 ? 1u : 2u);
+                }
+                if (MODE == kWeightsByQuery) {
+                    // a key behind the prompt may hold anything, and meets the tiles'
+                    // zero rows: its sum counts for nothing
+                    const int key = tile * 128 + row;
+                    if (key < p.N)
+                        p.part[(size_t)(2 * i + half) * p.B * p.Hkv * p.N + bg * p.N + key] =
+                            key < U.base + p.T ? l : 0.f;
+                    l = 0.f;
                 }
             }
             if (!ok) break;
             bc0 += U.n;
-            if (PASS == 1) {
-                const size_t rows = ((((size_t)U.b * p.Hkv + U.g) * p.nqt) + U.a) * 128 + row;
-                p.ml[rows * (2 * p.splits) + 2 * U.split + wg] = make_float2(m, l);
-            } else if (U.a * 128 + row < p.N) {
-                // a key behind the prompt may hold anything, and meets the tiles' zero
-                // rows: its sum counts for nothing
-                const int at = U.a * 128 + row;
-                if (at >= U.base + p.T) l = 0.f;
-                const size_t plane = (size_t)p.B * p.Hkv * p.N;
-                p.part[(2 * U.split + wg) * plane + ((size_t)U.b * p.Hkv + U.g) * p.N + at] = l;
+            if (active) cnt += U.n;
+            if (MODE == kWeightsByQuery && U.n > 0) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_a_empty);
+            }
+            if (MODE == kWeightsLse && active)
+                p.ml[((bg * p.nqt + U.a + i) * 128 + row) * (2 * p.splits) + 2 * U.split + half] = make_float2(m, l);
+            if (MODE == kWeightsByKey && active) {
+                const int key = (U.a + i) * 128 + row;
+                if (key < p.N)
+                    p.part[(size_t)(2 * U.split + half) * p.B * p.Hkv * p.N + bg * p.N + key] =
+                        key < U.base + p.T ? l : 0.f;
             }
         }
     }
@@ -309,8 +408,8 @@ swa_prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
     }
 }
 
-// Joins pass 1's partial {max, sum} of each row: -lse, or -infinity for a row
-// that is no query (so that its weights are 2^-inf = 0).
+// Joins the lse pass's partial {max, sum} of each row: -lse, or -infinity for a
+// row that is no query (so that its weights are 2^-inf = 0).
 __global__ void __launch_bounds__(128)
 swa_weights_lse_kernel(const float2 *__restrict__ ml, float *__restrict__ lse, const int32_t *__restrict__ lens, int N,
                        int T, int Hkv, int G, int TQ, int nqt, int parts) {
@@ -335,12 +434,21 @@ swa_weights_lse_kernel(const float2 *__restrict__ ml, float *__restrict__ lse, c
     lse[row] = out;
 }
 
-// weights[i] = the sum of the partial results, in order.
-__global__ void swa_weights_sum_kernel(const float *__restrict__ part, float *__restrict__ weights, long long n,
-                                       int parts) {
+// weights[i] = the sum of the partial planes, in order.  by_query: the planes
+// hold only the key tiles that the queries see.
+__global__ void swa_weights_sum_kernel(const WeightsParams p, float *__restrict__ weights, int planes, int by_query) {
+    const long long n = (long long)p.B * p.Hkv * p.N;
     for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
         float w = 0.f;
-        for (int s = 0; s < parts; ++s) w += __ldg(part + s * n + i);
+        bool there = true;
+        if (by_query) {
+            const int key = (int)(i % p.N), b = (int)(i / p.N / p.Hkv);
+            int lo, hi;
+            weights_key_tiles(p, weights_len(__ldg(p.lens + b), p.N) - p.T, 0, p.nqt - 1, lo, hi);
+            there = key / 128 >= lo && key / 128 <= hi;
+        }
+        if (there)
+            for (int s = 0; s < planes; ++s) w += __ldg(p.part + s * n + i);
         weights[i] = w;
     }
 }
