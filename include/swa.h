@@ -335,12 +335,16 @@ swa_status_t swa_cache_append_q8(const void *k_new, const void *v_new, void *k_c
                                  float *k_scale, float *v_scale, const int32_t *pos, int B, int T,
                                  int Hkv, int D, int W, int block, swa_stream_t stream);
 
-/* swa_decode_q8 -- swa_decode over the 8-bit buffer.  The workspace is that of
- * swa_decode: swa_decode_workspace_size(B, Hq, Hkv, D, W). */
+/* swa_decode_q8 -- swa_decode over the 8-bit buffer.  workspace: at least
+ * swa_decode_q8_workspace_size() bytes, 256-byte aligned, as for swa_decode;
+ * the size is 0, and workspace may be NULL, where the window is one split or
+ * its splits are merged on chip. */
 swa_status_t swa_decode_q8(const void *q, const void *k_cache, const void *v_cache,
                            const float *k_scale, const float *v_scale, const int32_t *pos, void *out,
                            int B, int Hq, int Hkv, int D, int W, int block, float scale,
                            void *workspace, size_t workspace_bytes, swa_stream_t stream);
+
+size_t swa_decode_q8_workspace_size(int B, int Hq, int Hkv, int D, int W);
 
 /* swa_prefill_chunk_q8 -- swa_prefill_chunk through the 8-bit buffer: query
  * s0+t attends to the cached positions in its window, as the codes stand for
@@ -393,7 +397,8 @@ swa_status_t swa_cache_evict_append(const void *k_new, const void *v_new, void *
  * weights NULL: from 0; weights_out may be weights.  A KV head that holds no
  * token gives an output of 0.  A sequence with pos[b] < 0 is skipped.
  * workspace: at least swa_decode_weights_workspace_size() bytes, 256-byte
- * aligned, as for swa_decode.  At most 2048 query heads to a KV head. */
+ * aligned, as for swa_decode; the size is 0, and workspace may be NULL, where
+ * the splits are merged on chip (small batches).  At most 2048 query heads to a KV head. */
 swa_status_t swa_decode_weights(const void *q, const void *k_cache, const void *v_cache,
                                 const int32_t *slot_pos, const float *weights, float *weights_out,
                                 const int32_t *pos, void *out, int B, int Hq, int Hkv, int D, int M,

@@ -24,6 +24,7 @@ __all__ = [
     "swa_selftest_wait_timeout", "swa_selftest_exp2", "SWA_OK", "SWA_ERR_INVALID_ARG",
     "SWA_ERR_UNSUPPORTED", "SWA_ERR_CUDA", "SWA_ERR_TIMEOUT", "SWA_WINDOW_EXCL_LEFT",
     "SWA_WINDOW_INCL_LEFT", "bounds_checked", "swa_cache_append_q8", "swa_decode_q8", "swa_prefill_chunk_q8",
+    "swa_decode_q8_workspace_size",
     "swa_prefill_chunk_q8_workspace_size", "swa_cache_evict_append", "swa_decode_weights",
     "swa_decode_weights_workspace_size", "swa_cache_keep", "swa_prefill_weights",
     "swa_prefill_weights_workspace_size",
@@ -151,7 +152,8 @@ def lib() -> ctypes.CDLL:
                 fn.restype = ctypes.c_int
             L.swa_prefill_chunk_q8_workspace_size.argtypes = [i] * 4
             L.swa_decode_weights_workspace_size.argtypes = [i] * 5
-            for fn in (L.swa_prefill_chunk_q8_workspace_size, L.swa_decode_weights_workspace_size):
+            L.swa_decode_q8_workspace_size.argtypes = [i] * 5
+            for fn in (L.swa_decode_q8_workspace_size, L.swa_prefill_chunk_q8_workspace_size, L.swa_decode_weights_workspace_size):
                 fn.restype = ctypes.c_size_t
             L.swa_decode_workspace_size.argtypes = [i, i, i, i, i]
             L.swa_decode_workspace_size.restype = ctypes.c_size_t
@@ -526,7 +528,7 @@ def swa_cache_append_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, pos, b
 def swa_decode_q8(q, k_cache, v_cache, k_scale, v_scale, pos, scale: float, block: int = 64, out=None, workspace=None,
                   stream=None):
     """swa_decode over an 8-bit buffer (swa_cache_append_q8).  q [B,Hq,D] bf16;
-    workspace as for swa_decode."""
+    workspace: swa_decode_q8_workspace_size bytes."""
     import torch
     dev = torch.cuda.current_device()
     cache, (B, W, Hkv, D) = _q8_cache(k_cache, v_cache, k_scale, v_scale, block, dev)
@@ -536,10 +538,14 @@ def swa_decode_q8(q, k_cache, v_cache, k_scale, v_scale, pos, scale: float, bloc
     if out is None:
         out = _empty(q, rows, torch.bfloat16, stream)
     L = lib()
-    workspace, ws, size = _scratch(workspace, L.swa_decode_workspace_size(B, Hq, Hkv, D, W), q, dev, stream)
+    workspace, ws, size = _scratch(workspace, L.swa_decode_q8_workspace_size(B, Hq, Hkv, D, W), q, dev, stream)
     _check(L.swa_decode_q8(*args, _ptr(out, "out", torch.bfloat16, rows, dev), B, Hq, Hkv, D, W, block, scale, ws, size,
                            _stream(stream, dev)), "swa_decode_q8")
     return out
+
+
+def swa_decode_q8_workspace_size(B: int, Hq: int, Hkv: int, D: int, W: int) -> int:
+    return int(lib().swa_decode_q8_workspace_size(B, Hq, Hkv, D, W))
 
 
 def swa_prefill_chunk_q8_workspace_size(B: int, Hkv: int, D: int, W: int) -> int:

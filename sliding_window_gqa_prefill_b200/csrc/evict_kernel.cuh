@@ -10,37 +10,60 @@
 
 namespace swa {
 
-// 16-byte copy, or 16 zero bytes where `there` is false (src is not read).
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+template <bool B>
+struct Flag {
+    static constexpr bool value = B;
+};
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
 // ---------------------------------------------------------------------------
 // Decode that keeps the scores.  As swa_decode_kernel over the slots
-// 0 .. min(pos+1, M)-1 that hold a position, and each block also writes its
-// scores (base 2, scaled; -inf for a free slot) to the workspace, from which
-// swa_weights_finish_kernel takes the weights once the softmax sums are known.
-// A score costs 4 bytes written and read per query head against the 4 D bytes
-// of K and V per KV head; at B=64, M=4096 they stay in L2.  Free slots
-// are copied as zeros, so what they hold never meets the products.
+// 0 .. min(pos+1, M)-1 that hold a position, and each block also keeps its
+// scores (base 2, scaled; -inf for a free slot), from which the weights follow
+// once the softmax sums are known.  What free slots hold never meets the
+// products: their scores are replaced, and in a 16-key block that has one (a
+// branch the whole warp takes) their values are cleared.  slot_pos comes through
+// the rings, 4 bytes per key beside the 4 D of K and V.
+//  * CLUSTER: the slots are cut over the 4 blocks of a cluster, the scores stay
+//    in shared memory, the sums are exchanged through distributed shared memory,
+//    and every block adds its own slots' weights: one launch, no workspace.
+//    The host takes it where all blocks run at once and the group is not cut:
+//    past that, the time a block spends on its weights is time its share of the
+//    memory system is idle (B=18, M=1000: 27.0 against 20.1 us; B=9: 16.0 both;
+//    3 sequences of 701 slots: 5.9 against 11.3).
+//  * else the scores (4 bytes written and read per slot and query head, against
+//    4 D bytes of K and V per KV head) and partial results go to the workspace
+//    and swa_weights_finish_kernel does the rest.
 template <int D, int G>
 struct DecodeScoresCfg {
     using Base = DecodeCfg<D, G>;
-    static constexpr int OFF_MASK = Base::SMEM_BYTES;            // one bit per key of the split
-    static constexpr int SMEM_BYTES = OFF_MASK + kDecodeSplit / 8;
+    static constexpr int ROW = D + 3;                            // {o[D], m, l, l of the rounded weights}
+    static constexpr int STAGE_BYTES = Base::STAGE_BYTES + kDecodeBlk * 4;      // K, V, slot_pos
+    static constexpr int WARP_RING = kDecodeStages * STAGE_BYTES;
+    static constexpr int OFF_HEAD = kDecodeWarps * WARP_RING;    // per head {m, 1 / l, 1 / l rounded}
+    static constexpr int OFF_SCORES = OFF_HEAD + 8 * 16;         // CLUSTER: [G][keys of the block]
+    static constexpr int SMEM_BYTES = OFF_SCORES;
+    static constexpr int MAX_SMEM = OFF_SCORES + kDecodeSplit * G * 4;
+    static_assert((kDecodeWarps + 1) * G * ROW * 4 <= OFF_HEAD, "the merge reuses the rings");
 };
 
-template <int D, int G>
+// weights_in, weights_out, out: CLUSTER only.  score_stride: slots per row of
+// scores (CLUSTER: per block, in shared memory).
+template <int D, int G, bool CLUSTER>
 __global__ void __launch_bounds__(kDecodeWarps * 32, 2)
 swa_decode_scores_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ kc,
                          const __nv_bfloat16 *__restrict__ vc, const int32_t *__restrict__ slot_pos,
                          const int32_t *__restrict__ pos, float4 *__restrict__ ws_ml, float *__restrict__ ws_o,
                          float *__restrict__ scores, int score_stride, int Hkv, int M, int nsplit_max,
-                         float scale_log2, int split_len, int kv_rep) {
+                         float scale_log2, int split_len, int kv_rep, const float *weights_in, float *weights_out,
+                         __nv_bfloat16 *__restrict__ out) {
     using Cfg = DecodeCfg<D, G>;
+    using SCfg = DecodeScoresCfg<D, G>;
     constexpr int CH = Cfg::CH, RB = Cfg::ROW_BYTES;
     extern __shared__ __align__(128) uint8_t smem[];
-    uint32_t *mask = reinterpret_cast<uint32_t *>(smem + DecodeScoresCfg<D, G>::OFF_MASK);
 
     const int split = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
     const int Hq = Hkv * G;
@@ -50,23 +73,19 @@ swa_decode_scores_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat1
         return;
     }
     const int L = (p >= M - 1) ? M : p + 1;
-    if ((long long)split * split_len >= L) return;
-    const int begin = split * split_len;
-    const int end = min(L, begin + split_len);
+    constexpr int kClusterKeys = kDecodeClusterSplits * kDecodeBlk;
+    const int split_keys = CLUSTER ? (L + kClusterKeys - 1) / kClusterKeys * kDecodeBlk : split_len;
+    // a cluster block past the last slot still takes part in the merge
+    if (!CLUSTER && (long long)split * split_keys >= L) return;
+    const int begin = (int)min((long long)split * split_keys, (long long)L);
+    const int end = min(L, begin + split_keys);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int hr = lane >> 2, t4 = lane & 3;
     const bool head_ok = hr < G;
-    const uint32_t ring = smem_addr(smem) + warp * Cfg::WARP_RING;
+    const uint32_t ring = smem_addr(smem) + warp * SCfg::WARP_RING;
     const int Hkv_mem = Hkv / kv_rep, gk = g / kv_rep;
-
-    // which slots of the split hold a token: bit i of word w is slot begin + 32 w + i
     const int32_t *sp = slot_pos + ((size_t)b * Hkv_mem + gk) * M;
-    for (int w = warp; w < (end - begin + 31) / 32; w += kDecodeWarps) {
-        const int key = begin + w * 32 + lane;
-        const uint32_t bits = __ballot_sync(0xffffffffu, key < end && in_bounds(key, M) && __ldg(sp + key) >= 0);
-        if (lane == 0) mask[w] = bits;
-    }
 
     uint32_t qa[Cfg::KSTEPS][2];
     {
@@ -81,28 +100,31 @@ swa_decode_scores_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat1
     const size_t row_stride = (size_t)Hkv_mem * D;
     const __nv_bfloat16 *kbase = kc + ((size_t)b * M * Hkv_mem + gk) * D;
     const __nv_bfloat16 *vbase = vc + ((size_t)b * M * Hkv_mem + gk) * D;
-    float *srow = scores + ((size_t)b * Hq + g * G + hr) * score_stride;
-    __syncthreads();
+    // this head's row of scores: in the workspace from slot 0, in shared memory
+    // from the block's first slot
+    float *srow = CLUSTER ? reinterpret_cast<float *>(smem + SCfg::OFF_SCORES) + hr * score_stride
+                          : scores + ((size_t)b * Hq + g * G + hr) * score_stride + begin;
 
     const int nblk = (end - begin + kDecodeBlk - 1) / kDecodeBlk;
     const int my_blocks = (nblk > warp) ? (nblk - warp + kDecodeWarps - 1) / kDecodeWarps : 0;
-    auto held = [&](int rel) -> uint32_t { return mask[rel >> 5] >> (rel & 31); };   // rel: a multiple of 16
 
     auto issue = [&](int i_local, int stage) {
-        const int rel = (warp + i_local * kDecodeWarps) * kDecodeBlk;
-        const uint32_t bits = held(rel);
-        const uint32_t st = ring + stage * Cfg::STAGE_BYTES;
+        const int key0 = begin + (warp + i_local * kDecodeWarps) * kDecodeBlk;
+        const uint32_t st = ring + stage * SCfg::STAGE_BYTES;
 #pragma unroll
         for (int c = 0; c < Cfg::CPL; ++c) {
             const int id = c * 32 + lane;
             const int r = id / CH, ch = id % CH;
-            const int key = min(begin + rel + r, end - 1);     // clamp: always in bounds
+            const int key = min(key0 + r, end - 1);            // clamp: always in bounds
             if (!in_bounds(key, M)) continue;
-            const bool there = (bits >> r) & 1u;
             const uint32_t off = swz_off(r, ch, RB);
             const size_t rowi = (size_t)key * row_stride + ch * 8;
-            cp_async16_zfill(st + off, kbase + rowi, there);
-            cp_async16_zfill(st + Cfg::BLK_BYTES + off, vbase + rowi, there);
+            cp_async16(st + off, kbase + rowi);
+            cp_async16(st + Cfg::BLK_BYTES + off, vbase + rowi);
+        }
+        if (lane < kDecodeBlk) {
+            const int key = min(key0 + lane, end - 1);
+            if (in_bounds(key, M)) cp_async4(st + Cfg::STAGE_BYTES + 4 * lane, sp + key);
         }
     };
 
@@ -126,9 +148,18 @@ swa_decode_scores_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat1
             if (nxt < my_blocks) issue(nxt, nxt % kDecodeStages);
             cp_async_commit();
         }
-        const uint32_t sk = ring + stage * Cfg::STAGE_BYTES, sv = sk + Cfg::BLK_BYTES;
+        const uint32_t sk = ring + stage * SCfg::STAGE_BYTES, sv = sk + Cfg::BLK_BYTES;
         const int rel = (warp + i * kDecodeWarps) * kDecodeBlk;
-        const uint32_t bits = held(rel) >> (2 * t4);       // bit 0, 1, 8, 9: this lane's keys
+        // which of the block's 16 slots hold a token; >> 2 t4: bit 0, 1, 8, 9 are
+        // this lane's keys
+        uint32_t held;
+        {
+            int32_t at = -1;
+            if (lane < kDecodeBlk && begin + rel + lane < end)
+                asm volatile("ld.shared.s32 %0, [%1];" : "=r"(at) : "r"(sk + Cfg::STAGE_BYTES + 4 * lane) : "memory");
+            held = __ballot_sync(0xffffffffu, at >= 0);
+        }
+        const uint32_t bits = held >> (2 * t4);
 
         float s[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
@@ -148,8 +179,8 @@ swa_decode_scores_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat1
             sc[e] = ((bits >> ((e & 1) + (e >> 1) * 8)) & 1u) ? sc[e] * scale_log2 : -INFINITY;
             mx = fmaxf(mx, sc[e]);
         }
-        if (head_ok && in_bounds(begin + rel + 15, score_stride)) {
-            float2 *dst = reinterpret_cast<float2 *>(srow + begin + rel + 2 * t4);
+        if (head_ok && in_bounds((CLUSTER ? 0 : begin) + rel + 15, score_stride)) {
+            float2 *dst = reinterpret_cast<float2 *>(srow + rel + 2 * t4);
             dst[0] = make_float2(sc[0], sc[1]);
             dst[4] = make_float2(sc[2], sc[3]);
         }
@@ -180,15 +211,25 @@ swa_decode_scores_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat1
         const uint32_t pa0 = pack_bf16x2(pw[0], pw[1]), pa2 = pack_bf16x2(pw[2], pw[3]);
         l_run += (pw[0] + pw[1]) + (pw[2] + pw[3]);
         lr2 = add_bf16x2(add_bf16x2(lr2, pa0), pa2);
+        auto add_pv = [&](auto masked) {
+            const uint32_t keep0 = ((bits & 1u) ? 0xFFFFu : 0u) | ((bits & 2u) ? 0xFFFF0000u : 0u);
+            const uint32_t keep1 = ((bits & 256u) ? 0xFFFFu : 0u) | ((bits & 512u) ? 0xFFFF0000u : 0u);
 #pragma unroll
-        for (int c2 = 0; c2 < CH / 2; ++c2) {
-            const int mi = lane >> 3;
-            const int r = (mi & 1) * 8 + (lane & 7), ch = c2 * 2 + (mi >> 1);
-            uint32_t vb[4];
-            ldsm_x4_trans(sv + swz_off(r, ch, RB), vb);
-            mma_rows8(o[2 * c2][0], o[2 * c2][1], pa0, pa2, vb[0], vb[1]);
-            mma_rows8(o[2 * c2 + 1][0], o[2 * c2 + 1][1], pa0, pa2, vb[2], vb[3]);
-        }
+            for (int c2 = 0; c2 < CH / 2; ++c2) {
+                const int mi = lane >> 3;
+                const int r = (mi & 1) * 8 + (lane & 7), ch = c2 * 2 + (mi >> 1);
+                uint32_t vb[4];
+                ldsm_x4_trans(sv + swz_off(r, ch, RB), vb);
+                if constexpr (decltype(masked)::value) {
+                    vb[0] &= keep0, vb[2] &= keep0;
+                    vb[1] &= keep1, vb[3] &= keep1;
+                }
+                mma_rows8(o[2 * c2][0], o[2 * c2][1], pa0, pa2, vb[0], vb[1]);
+                mma_rows8(o[2 * c2 + 1][0], o[2 * c2 + 1][1], pa0, pa2, vb[2], vb[3]);
+            }
+        };
+        if (held == 0xFFFFu) add_pv(Flag<false>{});
+        else add_pv(Flag<true>{});
         __syncwarp();
     }
     cp_async_wait<0>();
@@ -199,11 +240,12 @@ swa_decode_scores_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat1
         lr_run += __shfl_xor_sync(0xffffffffu, lr_run, x);
     }
 
-    // merge the warps in shared memory (over the rings) into the split's
-    // partial result {m, l, l of the rounded weights}, o[D] per head
-    constexpr int ROW = D + 3;
+    // merge the warps in shared memory (over the rings) into the block's
+    // {o[D], m, l, l of the rounded weights} per head
+    constexpr int ROW = SCfg::ROW;
     __syncthreads();
     float *mg = reinterpret_cast<float *>(smem);
+    float *part = mg + kDecodeWarps * G * ROW;      // [G][ROW], read by the cluster
     if (head_ok) {
         float *dst = mg + (warp * G + hr) * ROW;
 #pragma unroll
@@ -218,7 +260,6 @@ swa_decode_scores_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat1
         }
     }
     __syncthreads();
-    if (!in_bounds(split, nsplit_max)) return;
     for (int idx = threadIdx.x; idx < G * D; idx += blockDim.x) {
         const int h = idx / D, d = idx % D;
         float m = -INFINITY;
@@ -233,9 +274,69 @@ swa_decode_scores_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat1
             lr += src[D + 2] * sc;
             acc += src[d] * sc;
         }
-        const size_t slot = (((size_t)b * Hkv + g) * nsplit_max + split) * G + h;
-        ws_o[slot * D + d] = acc;
-        if (d == 0) ws_ml[slot] = make_float4(m, l, lr, 0.f);
+        if (CLUSTER) {
+            part[h * ROW + d] = acc;
+            if (d == 0) {
+                part[h * ROW + D] = m;
+                part[h * ROW + D + 1] = l;
+                part[h * ROW + D + 2] = lr;
+            }
+        } else if (in_bounds(split, nsplit_max)) {
+            const size_t slot = (((size_t)b * Hkv + g) * nsplit_max + split) * G + h;
+            ws_o[slot * D + d] = acc;
+            if (d == 0) ws_ml[slot] = make_float4(m, l, lr, 0.f);
+        }
+    }
+    if constexpr (CLUSTER) {
+        // every block of the cluster reaches both barriers: the only return above
+        // depends on b alone, which the cluster shares
+        cluster_sync_all();
+        float4 *head = reinterpret_cast<float4 *>(smem + SCfg::OFF_HEAD);
+        if (threadIdx.x < G) {
+            const uint32_t row = smem_addr(part + threadIdx.x * ROW + D);
+            float mr[kDecodeClusterSplits], m = -INFINITY, l = 0.f, lr = 0.f;
+#pragma unroll
+            for (int r = 0; r < kDecodeClusterSplits; ++r) {
+                mr[r] = ld_peer_f32(row, r);
+                m = fmaxf(m, mr[r]);
+            }
+            if (m == -INFINITY) m = 0.f;            // nothing held: every 2^(-inf - 0) is 0
+#pragma unroll
+            for (int r = 0; r < kDecodeClusterSplits; ++r) {
+                const float sc = ex2_approx(mr[r] - m);
+                l += ld_peer_f32(row + 4, r) * sc;
+                lr += ld_peer_f32(row + 8, r) * sc;
+            }
+            // a KV head without a token gives an output of 0
+            head[threadIdx.x] = make_float4(m, l == 0.f ? 0.f : 1.f / l, lr == 0.f ? 0.f : 1.f / lr, 0.f);
+        }
+        __syncthreads();
+        static_assert((G * D) % kDecodeClusterSplits == 0, "outputs per block");
+        constexpr int kPer = G * D / kDecodeClusterSplits;
+        const int i0 = (int)cluster_rank() * kPer;
+        for (int idx = i0 + threadIdx.x; idx < i0 + kPer; idx += blockDim.x) {
+            const int h = idx / D, d = idx % D;
+            const uint32_t row = smem_addr(part + h * ROW);
+            float acc = 0.f;
+#pragma unroll
+            for (int r = 0; r < kDecodeClusterSplits; ++r)
+                acc += ld_peer_f32(row + d * 4, r) * ex2_approx(ld_peer_f32(row + D * 4, r) - head[h].x);
+            const size_t oi = ((size_t)b * Hq + g * G + h) * D + d;
+            if (in_bounds((long long)oi, (long long)gridDim.z * Hq * D)) out[oi] = __float2bfloat16_rn(acc * head[h].z);
+        }
+        // the weights of this block's slots, and a share of the slots behind the
+        // last, which keep theirs
+        const size_t wrow = ((size_t)b * Hkv + g) * M;
+        const float *sc = reinterpret_cast<const float *>(smem + SCfg::OFF_SCORES);
+        for (int s = begin + threadIdx.x; s < end; s += blockDim.x) {
+            float w = weights_in ? weights_in[wrow + s] : 0.f;
+#pragma unroll
+            for (int h = 0; h < G; ++h) w += ex2_approx(sc[h * score_stride + s - begin] - head[h].x) * head[h].y;
+            weights_out[wrow + s] = w;
+        }
+        for (int s = L + split * blockDim.x + threadIdx.x; s < M; s += kDecodeClusterSplits * blockDim.x)
+            weights_out[wrow + s] = weights_in ? weights_in[wrow + s] : 0.f;
+        cluster_sync_all();                          // peers' shared memory stays until read
     }
 }
 
@@ -261,6 +362,22 @@ swa_weights_finish_kernel(const int32_t *__restrict__ pos, const float4 *__restr
     if (!in_bounds(nsplit - 1, nsplit_max)) return;
     const int gt = G / rep;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // this thread's four slots: their weights, and the scores of the first heads,
+    // on their way while the sums are joined (the rows of scores are padded to
+    // whole fours)
+    static_assert(kFinishSlots == 4 * kFinishThreads, "four slots per thread");
+    const size_t row = ((size_t)b * Hkv + g) * M;
+    const float *srow = scores + ((size_t)b * Hkv + g) * G * score_stride;
+    const long long s0 = (long long)blockIdx.x * kFinishSlots + 4 * threadIdx.x;
+    constexpr int kFirst = 4;
+    float w[4];
+    float4 first[kFirst];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = weights_in && s0 + i < M ? weights_in[row + s0 + i] : 0.f;
+#pragma unroll
+    for (int h = 0; h < kFirst; ++h)
+        first[h] = s0 < L && h < G ? __ldg(reinterpret_cast<const float4 *>(srow + (size_t)h * score_stride + s0))
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
     // partial results of head h: slot(h) + s * gt
     auto slot = [&](int h) -> size_t {
         return (((size_t)b * Hkv + g) * rep + h / gt) * nsplit_max * gt + h % gt;
@@ -297,18 +414,24 @@ swa_weights_finish_kernel(const int32_t *__restrict__ pos, const float4 *__restr
             acc += ws_o[(s0 + (size_t)s * gt) * D + d] * ex2_approx(ws_ml[s0 + (size_t)s * gt].x - head[h].x);
         out[((size_t)b * Hkv * G + g * G + h) * D + d] = __float2bfloat16_rn(acc * head[h].z);
     }
-    const size_t row = ((size_t)b * Hkv + g) * M;
-    const float *srow = scores + ((size_t)b * Hkv + g) * G * score_stride;
+    auto add = [&](const float4 &x, int h) {
+        const float m = head[h].x, inv = head[h].y;
+        w[0] += ex2_approx(x.x - m) * inv;
+        if (s0 + 1 < L) w[1] += ex2_approx(x.y - m) * inv;
+        if (s0 + 2 < L) w[2] += ex2_approx(x.z - m) * inv;
+        if (s0 + 3 < L) w[3] += ex2_approx(x.w - m) * inv;
+    };
+    if (s0 < L) {
 #pragma unroll
-    for (int i = 0; i < kFinishSlots / kFinishThreads; ++i) {
-        const long long s = (long long)blockIdx.x * kFinishSlots + i * kFinishThreads + threadIdx.x;
-        if (s >= M || !in_bounds(s, M)) break;
-        float w = weights_in ? weights_in[row + s] : 0.f;
-        if (s < L)
-            for (int h = 0; h < G; ++h)
-                w += ex2_approx(__ldg(srow + (size_t)h * score_stride + s) - head[h].x) * head[h].y;
-        weights_out[row + s] = w;
+        for (int h = 0; h < kFirst; ++h)
+            if (h < G) add(first[h], h);
+#pragma unroll 4
+        for (int h = kFirst; h < G; ++h)
+            add(__ldg(reinterpret_cast<const float4 *>(srow + (size_t)h * score_stride + s0)), h);
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (s0 + i < M && in_bounds(s0 + i, M)) weights_out[row + s0 + i] = w[i];
 }
 
 // ---------------------------------------------------------------------------
@@ -329,8 +452,12 @@ __device__ __forceinline__ uint32_t weight_order(float w) {
 // are read per slot; the kernel is bound by that and, for small batches, by
 // the latency of one pass.
 constexpr int kEvictThreads = 256;
+constexpr int kEvictBatch = 16;                     // slots loaded side by side per thread
 constexpr int kEvictMaxSlots = 1 << 30;             // the slot's 30 bits
 
+// VEC: M is a multiple of 4 and both arrays are 16-byte aligned, so four slots
+// come in one load (B=64, M=4096: 7.2 us; one slot at a time, four in flight, 10.0).
+template <bool VEC>
 __global__ void __launch_bounds__(kEvictThreads)
 swa_evict_append_kernel(const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new, uint4 *__restrict__ k_cache,
                         uint4 *__restrict__ v_cache, int32_t *__restrict__ slot_pos, float *__restrict__ weights,
@@ -338,29 +465,49 @@ swa_evict_append_kernel(const uint4 *__restrict__ k_new, const uint4 *__restrict
                         int S, int R) {
     __shared__ unsigned long long best_of[kEvictThreads / 32];
     const int g = blockIdx.x, b = blockIdx.y;
-    const int p = __ldg(pos + b);
     const size_t bg = (size_t)b * Hkv + g;
+    const int32_t *sp = slot_pos + bg * M;
+    const float *wt = weights + bg * M;
+    constexpr int V = VEC ? 4 : 1, LOADS = kEvictBatch / V;
+    const int p = __ldg(pos + b);
+    unsigned long long best = ~0ull;
+    for (int s0 = 0; s0 < M; s0 += kEvictThreads * kEvictBatch) {
+        int32_t at[kEvictBatch];
+        float w[kEvictBatch];
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {           // every load before the first use
+            const int s = s0 + (i * kEvictThreads + threadIdx.x) * V;
+            if constexpr (VEC) {
+                int4 a = make_int4(0, 0, 0, 0);
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (s < M) {
+                    a = *reinterpret_cast<const int4 *>(sp + s);
+                    x = *reinterpret_cast<const float4 *>(wt + s);
+                }
+                at[4 * i] = a.x, at[4 * i + 1] = a.y, at[4 * i + 2] = a.z, at[4 * i + 3] = a.w;
+                w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+            } else {
+                at[i] = s < M ? sp[s] : 0;
+                w[i] = s < M ? wt[s] : 0.f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kEvictBatch; ++i) {
+            const int s = s0 + (i / V * kEvictThreads + threadIdx.x) * V + i % V;
+            unsigned long long key = ~0ull;
+            if (at[i] >= S && (long long)at[i] <= (long long)p - R)
+                key = (2ull << 62) | ((unsigned long long)weight_order(w[i]) << 30) | (unsigned)s;
+            if (at[i] < 0) key = (1ull << 62) | (unsigned)s;
+            if (at[i] == p) key = (unsigned)s;
+            if (s < M) best = key < best ? key : best;
+        }
+    }
     if (p < 0) {                                    // invalid position: record, write nothing
         if (threadIdx.x == 0) {
             record_status(kStatusInvalid);
             if (slots) slots[bg] = -1;
         }
         return;
-    }
-    const int32_t *sp = slot_pos + bg * M;
-    const float *wt = weights + bg * M;
-    unsigned long long best = ~0ull;
-#pragma unroll 4
-    for (int s = threadIdx.x; s < M; s += kEvictThreads) {
-        const int at = sp[s];
-        const uint32_t w = weight_order(wt[s]);
-        unsigned long long key;
-        if (at == p) key = 0;
-        else if (at < 0) key = 1ull << 62;
-        else if (at >= S && (long long)at <= (long long)p - R) key = (2ull << 62) | ((unsigned long long)w << 30);
-        else continue;
-        key |= (unsigned long long)s;
-        best = key < best ? key : best;
     }
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) {
@@ -395,19 +542,28 @@ swa_evict_append_kernel(const uint4 *__restrict__ k_new, const uint4 *__restrict
 // The slots a prompt of n = lens[b] positions keeps in each KV head: all if
 // n <= M; else the first S, the last R and, between, the M - S - R of largest
 // weight (ties: the lowest position), in the order of their positions.  One
-// block per (sequence, KV head).  The smallest weight kept is found by four
-// passes over the middle positions, each fixing 8 bits of its order number by
-// a histogram (private to each warp, so the counts meet little contention);
-// then every warp counts, and after one exchange of the counts writes, the
-// positions it keeps in its own contiguous part of the prompt.
+// block per (sequence, KV head).  The smallest weight kept is found by three
+// passes over the middle positions, each fixing 11 (the last 10) bits of its
+// order number by a histogram; then every warp counts, and after one exchange of
+// the counts writes, the positions it keeps in its own contiguous part of the
+// prompt.  Digits of 11 bits, because weights lie in a few binades: with 8 bits
+// (sign and most of the exponent) the first pass put a warp's 32 counts on a
+// handful of addresses.  The order numbers stay in shared memory between the
+// passes where they fit.  N=16384, M=2048, 32 blocks: 8 bits and every pass from
+// L2 26.6 us, from shared memory 20.9, this 18.4 (and 11.8 for the copy of the rows).
 constexpr int kKeepThreads = 1024, kKeepWarps = kKeepThreads / 32;
-constexpr int kKeepSmem = (kKeepWarps * 256 + 256) * 4;
+constexpr int kKeepBins = 2048;
+constexpr int kKeepHists = 4;                       // each counted into by 8 warps
+constexpr int kKeepCached = 40 * 1024;
+inline int keep_smem(int N) { return (kKeepHists * kKeepBins + (N <= kKeepCached ? N : 0)) * 4; }
+constexpr int kKeepMaxSmem = (kKeepHists * kKeepBins + kKeepCached) * 4;
 
 __global__ void __launch_bounds__(kKeepThreads)
 swa_keep_select_kernel(const float *__restrict__ weights, const int32_t *__restrict__ lens,
                        int32_t *__restrict__ slot_pos, float *__restrict__ weights_out, int N, int Hkv, int M, int S,
                        int R) {
-    extern __shared__ uint32_t hist[];              // [warp][256], then the block's 256 sums
+    extern __shared__ uint32_t hist[];              // [kKeepHists][kKeepBins], then the order numbers
+    __shared__ uint32_t warp_sum[kKeepWarps];
     __shared__ uint32_t pick_digit, pick_left;
     __shared__ int2 part[kKeepWarps];               // per warp: {kept for sure, at the smallest weight}
     const int g = blockIdx.x, b = blockIdx.y;
@@ -431,50 +587,59 @@ swa_keep_select_kernel(const float *__restrict__ weights, const int32_t *__restr
     const int lo = S, hi = n - R;                   // the middle: n > M >= S + R, so it has more than M - S - R
     uint32_t left = (uint32_t)(M - S - R);          // still to choose among those that match `prefix`
     uint32_t prefix = 0, mask = 0;
-    uint32_t *sums = hist + kKeepWarps * 256;
+    uint32_t *cached = hist + kKeepHists * kKeepBins;
+    const bool cache = N <= kKeepCached;
+    if (cache) {
+#pragma unroll 8
+        for (int j = threadIdx.x; j < n; j += kKeepThreads) cached[j] = weight_order(__ldg(w + j));
+    }
+    auto order = [&](int j) -> uint32_t { return cache ? cached[j] : weight_order(__ldg(w + j)); };
     if (left > 0) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = threadIdx.x; i < kKeepWarps * 256; i += kKeepThreads) hist[i] = 0;
+#pragma unroll
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+            const uint32_t digits = pass == 2 ? 1023u : 2047u;
+            for (int i = threadIdx.x; i < kKeepHists * kKeepBins / 4; i += kKeepThreads)
+                reinterpret_cast<uint4 *>(hist)[i] = make_uint4(0, 0, 0, 0);
             __syncthreads();
+            uint32_t *mine = hist + (warp % kKeepHists) * kKeepBins;
+#pragma unroll 4
             for (int j = lo + threadIdx.x; j < hi; j += kKeepThreads) {
-                const uint32_t u = weight_order(__ldg(w + j));
-                if ((u & mask) == prefix) atomicAdd(&hist[warp * 256 + ((u >> shift) & 255)], 1u);
+                const uint32_t u = order(j);
+                if ((u & mask) == prefix) atomicAdd(&mine[(u >> shift) & digits], 1u);
             }
             __syncthreads();
-            if (threadIdx.x < 256) {
-                uint32_t c = 0;
-                for (int i = 0; i < kKeepWarps; ++i) c += hist[i * 256 + threadIdx.x];
-                sums[threadIdx.x] = c;
+            // thread t holds bins 2047 - 2t and 2046 - 2t, largest first
+            const int bin = kKeepBins - 2 - 2 * (int)threadIdx.x;
+            uint2 c = make_uint2(0, 0);              // .y the larger bin
+#pragma unroll
+            for (int i = 0; i < kKeepHists; ++i) {
+                const uint2 x = *reinterpret_cast<const uint2 *>(hist + i * kKeepBins + bin);
+                c.x += x.x;
+                c.y += x.y;
             }
+            uint32_t before = c.x + c.y;             // inclusive sum over the threads so far
+#pragma unroll
+            for (int x = 1; x < 32; x *= 2) {
+                const uint32_t o = __shfl_up_sync(0xffffffffu, before, x);
+                if (lane >= x) before += o;
+            }
+            if (lane == 31) warp_sum[warp] = before;
+            before -= c.x + c.y;
             __syncthreads();
-            if (warp == 0) {
-                // lane l holds digits 255 - 8l .. 248 - 8l, largest first
-                uint32_t c[8], mine = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    c[i] = sums[255 - 8 * lane - i];
-                    mine += c[i];
-                }
-                uint32_t before = mine;
-#pragma unroll
-                for (int x = 1; x < 32; x *= 2) {
-                    const uint32_t o = __shfl_up_sync(0xffffffffu, before, x);
-                    if (lane >= x) before += o;
-                }
-                before -= mine;                     // how many have a larger digit than this lane's
-                if (before < left && before + mine >= left) {
-                    int i = 0;
-                    while (before + c[i] < left) before += c[i++];
-                    pick_digit = 255 - 8 * lane - i;
-                    pick_left = left - before;
-                }
+            before += __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0u);
+            if (before < left && before + c.x + c.y >= left) {       // one thread: the counts reach `left` here
+                const bool upper = before + c.y >= left;
+                pick_digit = upper ? bin + 1 : bin;
+                pick_left = left - before - (upper ? 0 : c.y);
             }
             __syncthreads();
             prefix |= pick_digit << shift;
-            mask |= 255u << shift;
+            mask |= digits << shift;
             left = pick_left;
         }
     }
+    __syncthreads();
     // `prefix` is the smallest order number kept, `left` of its holders are
     // (lowest positions first); with nothing to choose, none
     const bool none = M - S - R == 0;
@@ -483,10 +648,11 @@ swa_keep_select_kernel(const float *__restrict__ weights, const int32_t *__restr
     auto kind = [&](int j) -> int {                 // 2: kept, 1: at the smallest weight kept, 0: not
         if (j < lo || j >= hi) return 2;
         if (none) return 0;
-        const uint32_t u = weight_order(__ldg(w + j));
+        const uint32_t u = order(j);
         return u > prefix ? 2 : u == prefix ? 1 : 0;
     };
     int sure = 0, tie = 0;
+#pragma unroll 4
     for (int j0 = w0; j0 < w1; j0 += 32) {
         const int k = j0 + lane < w1 ? kind(j0 + lane) : 0;
         sure += __popc(__ballot_sync(0xffffffffu, k == 2));
@@ -494,16 +660,15 @@ swa_keep_select_kernel(const float *__restrict__ weights, const int32_t *__restr
     }
     if (lane == 0) part[warp] = make_int2(sure, tie);
     __syncthreads();
-    int at = 0, ties = 0;
-    for (int i = 0; i < warp; ++i) {
-        at += part[i].x;
-        ties += part[i].y;
-    }
-    at += min(ties, (int)left);
+    const int2 ahead = lane < warp ? part[lane] : make_int2(0, 0);
+    int ties = __reduce_add_sync(0xffffffffu, ahead.y);
+    int at = __reduce_add_sync(0xffffffffu, ahead.x) + min(ties, (int)left);
     const uint32_t below = (1u << lane) - 1;
+#pragma unroll 4
     for (int j0 = w0; j0 < w1; j0 += 32) {
         const int j = j0 + lane;
         int k = j < w1 ? kind(j) : 0;
+        const float value = j < w1 ? __ldg(w + j) : 0.f;       // on its way before it is known to be kept
         const uint32_t tb = __ballot_sync(0xffffffffu, k == 1);
         if (k == 1 && ties + __popc(tb & below) >= (int)left) k = 0;
         const uint32_t kb = __ballot_sync(0xffffffffu, k != 0);
@@ -511,7 +676,7 @@ swa_keep_select_kernel(const float *__restrict__ weights, const int32_t *__restr
             const int s = at + __popc(kb & below);
             if (in_bounds(s, M)) {
                 sp[s] = j;
-                wo[s] = __ldg(w + j);
+                wo[s] = value;
             }
         }
         at += __popc(kb);

@@ -65,6 +65,14 @@ __device__ __forceinline__ float q8_scale(float top, float &inv) {
     return __uint_as_float((uint32_t)(127 + e) << 23);
 }
 
+// Two bf16 magnitudes at once: the larger of each half; a NaN in either half of
+// either operand stays one.
+__device__ __forceinline__ uint32_t bf16x2_max_nan(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // A bf16 value times the inverse scale, ready for the conversion to e4m3:
 // infinities become NaN (e4m3 has none, and 448 would hide them).
 __device__ __forceinline__ float q8_scaled(float x, float inv) {
@@ -79,6 +87,54 @@ __host__ __device__ inline int q8_blocks_touched(int T, int block, int nblk) {
     return n < nblk ? (int)n : nblk;
 }
 
+// The larger of `top` and the magnitudes of 8 bf16 (two halves kept apart).
+__device__ __forceinline__ uint32_t q8_top(uint32_t top, const uint4 &x) {
+    top = bf16x2_max_nan(bf16x2_max_nan(top, x.x & 0x7FFF7FFFu), x.y & 0x7FFF7FFFu);
+    return bf16x2_max_nan(bf16x2_max_nan(top, x.z & 0x7FFF7FFFu), x.w & 0x7FFF7FFFu);
+}
+
+// The largest finite magnitude of 8 bf16, element by element (rare: where
+// q8_top met a NaN or an infinity).
+__device__ __forceinline__ uint32_t q8_top_finite(uint32_t top, const uint4 &x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t lo = w[e] & 0x7FFFu, hi = (w[e] >> 16) & 0x7FFFu;
+        top = max(top, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+    }
+    return top;
+}
+
+// 8 bf16 as codes.  finite: none of the thread's elements is a NaN or infinite.
+__device__ __forceinline__ uint2 q8_codes(const uint4 &x, float inv, bool finite) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t c[4];
+    if (finite) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            c[e] = f32x2_to_e4m3x2(__uint_as_float(w[e] << 16) * inv, __uint_as_float(w[e] & 0xFFFF0000u) * inv);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            c[e] = f32x2_to_e4m3x2(q8_scaled(__uint_as_float(w[e] << 16), inv),
+                                   q8_scaled(__uint_as_float(w[e] & 0xFFFF0000u), inv));
+    }
+    return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// The largest value of `v` over the thread block.
+template <int WARPS>
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t *red) {
+    v = __reduce_max_sync(0xffffffffu, v);
+    if (WARPS > 1) {
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+        __syncthreads();
+        const int lane = threadIdx.x & 31;
+        v = __reduce_max_sync(0xffffffffu, lane < WARPS ? red[lane] : 0u);
+    }
+    return v;
+}
+
 // Append.  One thread block owns one (cache block, KV head, K or V) of one
 // sequence, so nothing is shared and no atomic is needed: it reads the new
 // tokens of its slots and the codes that stay, takes the largest magnitude of
@@ -87,6 +143,12 @@ __host__ __device__ inline int q8_blocks_touched(int T, int block, int nblk) {
 // count for nothing and stay as they are.  Each thread holds 4 pieces of 8
 // elements (16 bytes of bf16, 8 of codes), so the block is read once and
 // stays in registers between the maximum and the rounding.
+//
+// Bound by memory for long appends if the arithmetic per piece stays small: 4 x
+// 4000 tokens, 8 heads, D=128 (99 MB): 31 us with one path for every block and
+// scalar maxima (170 instructions a piece), 23.3 with packed maxima, 18.3 with
+// whole blocks apart.  A step of one token for 64 sequences takes 7.5 us, mostly
+// the latency of position -> block -> scale.
 template <int BLOCK, int D>
 __global__ void __launch_bounds__(BLOCK * D / 32)
 swa_append_q8_kernel(const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new,
@@ -96,7 +158,8 @@ swa_append_q8_kernel(const uint4 *__restrict__ k_new, const uint4 *__restrict__ 
     constexpr int PIECES = D / 8;             // 8-element pieces per row
     constexpr int ROWS = BLOCK / 4;           // rows per pass, 4 passes
     constexpr int WARPS = BLOCK * D / 1024;
-    __shared__ uint32_t red[2][WARPS > 0 ? WARPS : 1];
+    static_assert(WARPS >= 1 && WARPS <= 32, "whole warps");
+    __shared__ uint32_t red[2][WARPS];
     const int b = blockIdx.y;
     // heads and K / V vary fastest: the rows of one slot are read together
     const int hv = blockIdx.x % (2 * Hkv), i_blk = blockIdx.x / (2 * Hkv);
@@ -111,46 +174,73 @@ swa_append_q8_kernel(const uint4 *__restrict__ k_new, const uint4 *__restrict__ 
     int blk = first / BLOCK + i_blk;
     if (blk >= nblk) blk -= nblk;
     if (!in_bounds(blk, nblk) || i_blk >= ntouch) return;
-
-    const uint4 *src = is_v ? v_new : k_new;
-    uint2 *cache = is_v ? v_cache : k_cache;
-    float *sc = (is_v ? v_scale : k_scale) + ((size_t)b * nblk + blk) * Hkv + h;
-    const float old_scale = *sc;
+    // the block's slots s0 .. s1-1, and the token t0 that would go to the first
+    const int s0 = blk * BLOCK, s1 = min(W, s0 + BLOCK);
+    int t0 = s0 - first;
+    if (t0 < 0) t0 += W;
+    if (t0 >= T && !(first >= s0 && first < s1)) return;          // no new token here
 
     const int piece = threadIdx.x % PIECES, r0 = threadIdx.x / PIECES;
-    uint4 fresh[4];
-    uint2 held[4];
+    const size_t slot_pieces = (size_t)Hkv * PIECES;
+    const uint4 *src = (is_v ? v_new : k_new) + ((size_t)b * T * Hkv + h) * PIECES + piece;
+    uint2 *cache = (is_v ? v_cache : k_cache) + ((size_t)b * W * Hkv + h) * PIECES + piece;
+    float *sc = (is_v ? v_scale : k_scale) + ((size_t)b * nblk + blk) * Hkv + h;
+    uint4 x[4];                               // 8 bf16, or 8 codes in .x, .y
+    uint32_t top_new = 0;                     // magnitude, as bf16 bits
+    float inv;
+
+    // a block that new tokens fill needs nothing of what it held: most blocks of
+    // a long append, so it has code of its own
+    if ((long long)t0 + BLOCK <= T && s0 + BLOCK <= W) {
+        src += (size_t)(t0 + r0) * slot_pieces;
+        cache += (size_t)(s0 + r0) * slot_pieces;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = __ldg(src + (size_t)(i * ROWS) * slot_pieces);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top_new = q8_top(top_new, x[i]);
+        top_new = max(top_new & 0xFFFFu, top_new >> 16);
+        const bool finite = top_new < 0x7F80u;
+        if (!finite) {
+            top_new = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top_new = q8_top_finite(top_new, x[i]);
+        }
+        top_new = block_max<WARPS>(top_new, red[0]);
+        const float scale = q8_scale(__uint_as_float(top_new << 16), inv);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (in_bounds(s0 + r0 + i * ROWS, W))
+                cache[(size_t)(i * ROWS) * slot_pieces] = q8_codes(x[i], inv, finite);
+        if (threadIdx.x == 0) *sc = scale;
+        return;
+    }
+
+    const float old_scale = *sc;
     int state[4];                             // 0: leave alone, 1: holds a token, 2: new token
-    uint32_t top_new = 0, top_old = 0;        // magnitudes: bf16 bits, e4m3 bits
-    int any = 0;
+    uint32_t top_old = 0;                     // magnitude, as e4m3 bits
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int slot = blk * BLOCK + i * ROWS + r0;
+        const int slot = s0 + i * ROWS + r0;
         state[i] = 0;
         if (slot >= W) continue;
         int t = slot - first;
         if (t < 0) t += W;
         if (t < T) {
             state[i] = 2;
-            any = 1;
-            fresh[i] = __ldg(src + (((size_t)b * T + t) * Hkv + h) * PIECES + piece);
+            x[i] = __ldg(src + (size_t)t * slot_pieces);
         } else if (slot < p0) {
             state[i] = 1;
-            held[i] = cache[(((size_t)b * W + slot) * Hkv + h) * PIECES + piece];
+            const uint2 c = cache[(size_t)slot * slot_pieces];
+            x[i].x = c.x;
+            x[i].y = c.y;
         }
     }
-    if (!__syncthreads_or(any)) return;       // the last of `ntouch` blocks may be untouched
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (state[i] == 2) {
-            const uint32_t w[4] = {fresh[i].x, fresh[i].y, fresh[i].z, fresh[i].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t lo = w[e] & 0x7FFFu, hi = (w[e] >> 16) & 0x7FFFu;
-                top_new = max(top_new, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
-            }
+            top_new = q8_top(top_new, x[i]);
         } else if (state[i] == 1) {
-            const uint32_t w[2] = {held[i].x & 0x7F7F7F7Fu, held[i].y & 0x7F7F7F7Fu};
+            const uint32_t w[2] = {x[i].x & 0x7F7F7F7Fu, x[i].y & 0x7F7F7F7Fu};
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const uint32_t c = (w[e >> 2] >> (8 * (e & 3))) & 0x7Fu;
@@ -158,50 +248,42 @@ swa_append_q8_kernel(const uint4 *__restrict__ k_new, const uint4 *__restrict__ 
             }
         }
     }
-    top_new = __reduce_max_sync(0xffffffffu, top_new);
-    top_old = __reduce_max_sync(0xffffffffu, top_old);
-    if (WARPS > 1) {
-        if ((threadIdx.x & 31) == 0) {
-            red[0][threadIdx.x >> 5] = top_new;
-            red[1][threadIdx.x >> 5] = top_old;
-        }
-        __syncthreads();
+    top_new = max(top_new & 0xFFFFu, top_new >> 16);
+    const bool finite = top_new < 0x7F80u;    // of this thread's new elements
+    if (!finite) {
+        top_new = 0;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-            top_new = max(top_new, red[0][w]);
-            top_old = max(top_old, red[1][w]);
-        }
+        for (int i = 0; i < 4; ++i)
+            if (state[i] == 2) top_new = q8_top_finite(top_new, x[i]);
     }
+    top_new = block_max<WARPS>(top_new, red[0]);
+    top_old = block_max<WARPS>(top_old, red[1]);
     // the scale of a block that holds nothing yet may be anything: used only
     // where a held code is not zero
     float top = __uint_as_float(top_new << 16);
     if (top_old) top = fmaxf(top, f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)top_old)).x * old_scale);
-    float inv;
     const float scale = q8_scale(top, inv);
     const bool moved = scale != old_scale;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (state[i] == 0 || (state[i] == 1 && !moved)) continue;
-        const int slot = blk * BLOCK + i * ROWS + r0;
+        const int slot = s0 + i * ROWS + r0;
         if (!in_bounds(slot, W)) continue;
-        uint32_t c[4];
+        uint2 codes;
         if (state[i] == 2) {
-            const uint32_t w[4] = {fresh[i].x, fresh[i].y, fresh[i].z, fresh[i].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                c[e] = f32x2_to_e4m3x2(q8_scaled(__uint_as_float(w[e] << 16), inv),
-                                       q8_scaled(__uint_as_float(w[e] & 0xFFFF0000u), inv));
+            codes = q8_codes(x[i], inv, finite);
         } else {
-            const uint32_t w[2] = {held[i].x, held[i].y};
+            const uint32_t w[2] = {x[i].x, x[i].y};
+            uint32_t c[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float2 x = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(w[e >> 1] >> (16 * (e & 1)))));
+                const float2 v = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(w[e >> 1] >> (16 * (e & 1)))));
                 // two products, not one by old_scale * inv: that may overflow
-                c[e] = f32x2_to_e4m3x2(x.x * old_scale * inv, x.y * old_scale * inv);
+                c[e] = f32x2_to_e4m3x2(v.x * old_scale * inv, v.y * old_scale * inv);
             }
+            codes = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
         }
-        cache[(((size_t)b * W + slot) * Hkv + h) * PIECES + piece] =
-            make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+        cache[(size_t)slot * slot_pieces] = codes;
     }
     if (threadIdx.x == 0 && moved) *sc = scale;
 }

@@ -122,6 +122,8 @@ swa_status_t device_info(DeviceInfo **out) {
         SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_prefill_kernel<128>,
                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           swa::PrefillCfg<128>::SMEM_ALLOC));
+        SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_keep_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          swa::kKeepMaxSmem));
 #define SWA_SET_WEIGHTS_ATTR(DD, PP)                                                          \
     SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_prefill_weights_kernel<DD, PP>,               \
                                       cudaFuncAttributeMaxDynamicSharedMemorySize,           \
@@ -148,9 +150,12 @@ swa_status_t device_info(DeviceInfo **out) {
     SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_decode_q8_kernel<DD, GG, swa::kDecodeWindowCluster>, \
                                       cudaFuncAttributeMaxDynamicSharedMemorySize,           \
                                       swa::DecodeQ8Cfg<DD, GG>::SMEM_BYTES));                \
-    SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_decode_scores_kernel<DD, GG>,                 \
+    SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_decode_scores_kernel<DD, GG, false>,          \
                                       cudaFuncAttributeMaxDynamicSharedMemorySize,           \
-                                      swa::DecodeScoresCfg<DD, GG>::SMEM_BYTES));
+                                      swa::DecodeScoresCfg<DD, GG>::SMEM_BYTES));            \
+    SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_decode_scores_kernel<DD, GG, true>,           \
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize,           \
+                                      swa::DecodeScoresCfg<DD, GG>::MAX_SMEM));
         SWA_SET_DECODE_ATTR(64, 1) SWA_SET_DECODE_ATTR(64, 2) SWA_SET_DECODE_ATTR(64, 3)
         SWA_SET_DECODE_ATTR(64, 4) SWA_SET_DECODE_ATTR(64, 5) SWA_SET_DECODE_ATTR(64, 6)
         SWA_SET_DECODE_ATTR(64, 7) SWA_SET_DECODE_ATTR(64, 8)
@@ -727,6 +732,17 @@ swa_status_t launch_decode_q8_dg(const void *q, const void *kc, const void *vc, 
         default: return SWA_ERR_UNSUPPORTED;                                    \
     }
 
+// That of decode, or 0 where the window is one split or the splits are merged on
+// chip (or the sizes are invalid).
+size_t decode_q8_workspace_bytes(int B, int Hq, int Hkv, int D, int W) {
+    const size_t bytes = decode_workspace_bytes(B, Hq, Hkv, D, W);
+    if (bytes == 0) return 0;
+    int rep = 1;
+    decode_group(Hq, Hkv, &rep);
+    const int nsm = decode_nsplit_max(B, Hkv * rep, W);
+    return nsm == 1 || nsm == swa::kDecodeClusterSplits ? 0 : bytes;
+}
+
 swa_status_t decode_q8_impl(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
                             const float *v_scale, const int32_t *pos, void *out, int B, int Hq, int Hkv, int D,
                             int W, int block, float scale, void *workspace, size_t workspace_bytes, cudaStream_t s) {
@@ -734,10 +750,8 @@ swa_status_t decode_q8_impl(const void *q, const void *k_cache, const void *v_ca
     if (swa_status_t e = q8_cache_checks(k_cache, v_cache, k_scale, v_scale, pos, B, Hkv, D, W, block)) return e;
     int rep = 1;
     const int G = decode_group(Hq, Hkv, &rep);
-    if (decode_nsplit_max(B, Hkv * rep, W) > 1) {
-        if (!workspace || workspace_bytes < decode_workspace_bytes(B, Hq, Hkv, D, W) || misaligned(workspace, 256))
-            return SWA_ERR_INVALID_ARG;
-    }
+    const size_t need = decode_q8_workspace_bytes(B, Hq, Hkv, D, W);
+    if (need > 0 && (!workspace || workspace_bytes < need || misaligned(workspace, 256))) return SWA_ERR_INVALID_ARG;
     DeviceInfo *dev = nullptr;
     if (swa_status_t e = device_info(&dev)) return e;
     SWA_DISPATCH_DG(launch_decode_q8_dg, D, G, q, k_cache, v_cache, k_scale, v_scale, pos, out, B, Hkv * rep, W, block,
@@ -807,10 +821,31 @@ bool scores_supported(int B, int Hq, int Hkv, int M) {
     return B <= 65535 && (long long)Hkv * rep <= 65535 && Hq / Hkv <= kMaxFinishHeads && M <= swa::kEvictMaxSlots;
 }
 
+// Slots of one block of the cluster form, and whether a call takes that form:
+// the group in one piece, at most kDecodeSplit slots to a block, and no more
+// blocks than run at once (two to an SM where their shared memory fits, 115712
+// bytes each).
+int scores_cluster_keys(int M) {
+    constexpr int k = swa::kDecodeClusterSplits * swa::kDecodeBlk;
+    return (int)(((long long)M + k - 1) / k * swa::kDecodeBlk);
+}
+
+template <int D, int G>
+int scores_cluster_smem(int M) { return swa::DecodeScoresCfg<D, G>::OFF_SCORES + scores_cluster_keys(M) * G * 4; }
+
+bool scores_in_cluster(int B, int Hkv, int G, int rep, int D, int M) {
+    if (rep != 1 || scores_cluster_keys(M) > swa::kDecodeSplit) return false;
+    const int ring = D == 128 ? swa::DecodeScoresCfg<128, 1>::OFF_SCORES : swa::DecodeScoresCfg<64, 1>::OFF_SCORES;
+    const int smem = ring + scores_cluster_keys(M) * G * 4;
+    return (long long)B * Hkv * swa::kDecodeClusterSplits <= (smem <= 115712 ? 2 : 1) * 148;
+}
+
+// 0 where the merge is on chip (or the sizes are invalid).
 size_t decode_weights_workspace_bytes(int B, int Hq, int Hkv, int D, int M) {
     if (B < 1 || M < 1 || check_heads(Hq, Hkv, D) != SWA_OK || !scores_supported(B, Hq, Hkv, M)) return 0;
     int rep = 1;
-    decode_group(Hq, Hkv, &rep);
+    const int G = decode_group(Hq, Hkv, &rep);
+    if (scores_in_cluster(B, Hkv, G, rep, D, M)) return 0;
     return scores_layout(B, Hq, Hkv * rep, D, M).bytes;
 }
 
@@ -818,22 +853,43 @@ template <int D, int G>
 swa_status_t launch_decode_weights_dg(const void *q, const void *kc, const void *vc, const int32_t *slot_pos,
                                       const float *weights, float *weights_out, const int32_t *pos, void *out, int B,
                                       int groups, int M, float scale, void *ws, int rep, cudaStream_t s) {
+    const __nv_bfloat16 *qb = static_cast<const __nv_bfloat16 *>(q), *kb = static_cast<const __nv_bfloat16 *>(kc),
+                        *vb = static_cast<const __nv_bfloat16 *>(vc);
+    __nv_bfloat16 *ob = static_cast<__nv_bfloat16 *>(out);
+    float4 *ws_ml = nullptr;
+    float *ws_o = nullptr, *scores = nullptr;
+    if (scores_in_cluster(B, groups, G, rep, D, M)) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(swa::kDecodeClusterSplits, groups, B);
+        cfg.blockDim = dim3(swa::kDecodeWarps * 32);
+        cfg.dynamicSmemBytes = scores_cluster_smem<D, G>(M);
+        cfg.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = swa::kDecodeClusterSplits;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        SWA_CUDA_TRY(cudaLaunchKernelEx(&cfg, swa::swa_decode_scores_kernel<D, G, true>, qb, kb, vb, slot_pos, pos,
+                                        ws_ml, ws_o, scores, scores_cluster_keys(M), groups, M, 1, scale * kLog2e, 0,
+                                        rep, weights, weights_out, ob));
+        return SWA_OK;
+    }
     const ScoresLayout l = scores_layout(B, groups * G, groups, D, M);
     char *base = static_cast<char *>(ws);
-    float *ws_o = reinterpret_cast<float *>(base);
-    float4 *ws_ml = reinterpret_cast<float4 *>(base + l.ml_off);
-    float *scores = reinterpret_cast<float *>(base + l.scores_off);
-    swa::swa_decode_scores_kernel<D, G>
+    ws_o = reinterpret_cast<float *>(base);
+    ws_ml = reinterpret_cast<float4 *>(base + l.ml_off);
+    scores = reinterpret_cast<float *>(base + l.scores_off);
+    swa::swa_decode_scores_kernel<D, G, false>
         <<<dim3(l.nsm, groups, B), swa::kDecodeWarps * 32, swa::DecodeScoresCfg<D, G>::SMEM_BYTES, s>>>(
-            static_cast<const __nv_bfloat16 *>(q), static_cast<const __nv_bfloat16 *>(kc),
-            static_cast<const __nv_bfloat16 *>(vc), slot_pos, pos, ws_ml, ws_o, scores, l.stride, groups, M, l.nsm,
-            scale * kLog2e, l.split, rep);
+            qb, kb, vb, slot_pos, pos, ws_ml, ws_o, scores, l.stride, groups, M, l.nsm, scale * kLog2e, l.split, rep,
+            nullptr, nullptr, nullptr);
     SWA_CUDA_TRY(cudaGetLastError());
     const int Hkv = groups / rep, Gall = G * rep;
     swa::swa_weights_finish_kernel<<<dim3((M + swa::kFinishSlots - 1) / swa::kFinishSlots, Hkv, B),
                                      swa::kFinishThreads, Gall * sizeof(float4), s>>>(
-        pos, ws_ml, ws_o, scores, l.stride, weights, weights_out, static_cast<__nv_bfloat16 *>(out), Hkv, Gall, rep, D,
-        M, l.nsm, l.split);
+        pos, ws_ml, ws_o, scores, l.stride, weights, weights_out, ob, Hkv, Gall, rep, D, M, l.nsm, l.split);
     SWA_CUDA_TRY(cudaGetLastError());
     return SWA_OK;
 }
@@ -846,9 +902,8 @@ swa_status_t decode_weights_impl(const void *q, const void *k_cache, const void 
     if (!slot_pos || !weights_out || misaligned(slot_pos, 4) || misaligned(weights, 4) || misaligned(weights_out, 4))
         return SWA_ERR_INVALID_ARG;
     if (!scores_supported(B, Hq, Hkv, M)) return SWA_ERR_UNSUPPORTED;
-    if (!workspace || misaligned(workspace, 256) ||
-        workspace_bytes < decode_weights_workspace_bytes(B, Hq, Hkv, D, M))
-        return SWA_ERR_INVALID_ARG;
+    const size_t need = decode_weights_workspace_bytes(B, Hq, Hkv, D, M);
+    if (need > 0 && (!workspace || misaligned(workspace, 256) || workspace_bytes < need)) return SWA_ERR_INVALID_ARG;
     int rep = 1;
     const int G = decode_group(Hq, Hkv, &rep);
     DeviceInfo *dev = nullptr;
@@ -874,7 +929,9 @@ swa_status_t evict_append_impl(const void *k_new, const void *v_new, void *k_cac
         misaligned(slot_pos, 4) || misaligned(weights, 4) || misaligned(pos, 4) || misaligned(slots, 4))
         return SWA_ERR_INVALID_ARG;
     if (swa_status_t e = budget_checks(B, Hkv, D, M, S, R)) return e;
-    swa::swa_evict_append_kernel<<<dim3(Hkv, B), swa::kEvictThreads, 0, s>>>(
+    const bool vec = M % 4 == 0 && aligned16(slot_pos) && aligned16(weights);
+    auto kernel = vec ? swa::swa_evict_append_kernel<true> : swa::swa_evict_append_kernel<false>;
+    kernel<<<dim3(Hkv, B), swa::kEvictThreads, 0, s>>>(
         static_cast<const uint4 *>(k_new), static_cast<const uint4 *>(v_new), static_cast<uint4 *>(k_cache),
         static_cast<uint4 *>(v_cache), slot_pos, weights, pos, slots, Hkv, M, D / 8, S, R);
     SWA_CUDA_TRY(cudaGetLastError());
@@ -891,7 +948,7 @@ swa_status_t keep_impl(const void *k, const void *v, const float *weights, const
     if (swa_status_t e = budget_checks(B, Hkv, D, M, S, R)) return e;
     DeviceInfo *dev = nullptr;
     if (swa_status_t e = device_info(&dev)) return e;
-    swa::swa_keep_select_kernel<<<dim3(Hkv, B), swa::kKeepThreads, swa::kKeepSmem, s>>>(
+    swa::swa_keep_select_kernel<<<dim3(Hkv, B), swa::kKeepThreads, swa::keep_smem(N), s>>>(
         weights, lens, slot_pos, weights_out, N, Hkv, M, S, R);
     SWA_CUDA_TRY(cudaGetLastError());
     long long blocks = ((long long)B * M * Hkv * (D / 8) + 255) / 256;
@@ -1214,6 +1271,10 @@ swa_status_t swa_decode_q8(const void *q, const void *k_cache, const void *v_cac
                            int block, float scale, void *workspace, size_t workspace_bytes, swa_stream_t stream) {
     return decode_q8_impl(q, k_cache, v_cache, k_scale, v_scale, pos, out, B, Hq, Hkv, D, W, block, scale, workspace,
                           workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t swa_decode_q8_workspace_size(int B, int Hq, int Hkv, int D, int W) {
+    return decode_q8_workspace_bytes(B, Hq, Hkv, D, W);
 }
 
 size_t swa_prefill_chunk_q8_workspace_size(int B, int Hkv, int D, int W) {

@@ -46,6 +46,10 @@ def test_decode_q8(lib):
         ({7: 0}, BAD), ({8: 3}, BAD), ({9: 0}, BAD), ({10: 96}, UNSUP), ({11: 0}, BAD), ({12: 24}, BAD),
         ({13: 0.0}, BAD), ({13: float("nan")}, BAD), ({13: float("inf")}, BAD), ({14: None}, BAD), ({14: P + 128}, BAD),
         ({15: 16}, BAD), ({7: 65536}, UNSUP)])
+    size = lib.swa_decode_q8_workspace_size
+    assert size(1, 4, 2, 64, 600) >= 3 * 4 * 64 * 4                       # 3 splits
+    assert size(1, 4, 2, 64, 200) == size(64, 32, 8, 128, 4096) == 0      # one split; merged in the cluster
+    assert size(1, 3, 2, 64, 600) == size(0, 4, 2, 64, 600) == size(1, 4, 2, 72, 600) == 0
 
 
 def test_prefill_chunk_q8(lib):
@@ -70,13 +74,17 @@ def test_evict_append(lib):
 
 def test_decode_weights(lib):
     #        q  kc vc at w  wo pos out B  Hq Hkv D  M  scale ws bytes stream
-    good = [P] * 8 + [1, 4, 2, 64, 600, 0.1, P, 1 << 30, None]
+    good = [P] * 8 + [1, 4, 2, 64, 6000, 0.1, P, 1 << 30, None]
     vary(lib.swa_decode_weights, good, pointers(8, optional=(4,)) + [
         ({8: 0}, BAD), ({9: 3}, BAD), ({10: 0}, BAD), ({11: 96}, UNSUP), ({12: 0}, BAD), ({13: 0.0}, BAD),
         ({14: None}, BAD), ({14: P + 64}, BAD), ({15: 16}, BAD), ({9: 4098}, UNSUP), ({8: 65536}, UNSUP)])
     size = lib.swa_decode_weights_workspace_size
-    assert size(1, 4, 2, 64, 600) >= 4 * 600 * 4
-    assert size(1, 3, 2, 64, 600) == size(0, 4, 2, 64, 600) == size(1, 4, 2, 72, 600) == size(1, 4098, 2, 64, 600) == 0
+    assert size(1, 4, 2, 64, 6000) >= 4 * 6000 * 4
+    assert size(1, 24, 2, 64, 600) >= 24 * 600 * 4          # a group of 12 runs in two pieces
+    assert size(64, 32, 8, 128, 4096) >= 64 * 32 * 4096 * 4  # more blocks than run at once
+    # merged on chip
+    assert size(1, 4, 2, 64, 600) == size(9, 32, 8, 128, 4096) == size(4, 64, 8, 128, 4096) == 0
+    assert size(1, 3, 2, 64, 6000) == size(0, 4, 2, 64, 6000) == size(1, 4, 2, 72, 6000) == size(1, 4098, 2, 64, 6000) == 0
 
 
 def test_keep(lib):

@@ -364,7 +364,7 @@ def test_graph_replay_of_a_decode_step():
     k, v = rows(rng, B, 1, H, D), rows(rng, B, 1, H, D)
     q = rows(rng, B, Hq, D, spread=False)
     out = torch.empty_like(q)
-    ws = torch.empty(swa.swa_decode_workspace_size(B, Hq, H, D, W), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(swa.swa_decode_q8_workspace_size(B, Hq, H, D, W), dtype=torch.uint8, device="cuda")
 
     def step(buf, out):
         swa.swa_cache_append_q8(k, v, *buf.args(), pos, block=block)
