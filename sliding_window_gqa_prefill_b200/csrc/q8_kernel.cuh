@@ -289,8 +289,11 @@ swa_append_q8_kernel(const uint4 *__restrict__ k_new, const uint4 *__restrict__ 
 }
 
 // The cached window widened to bf16 (exact) for the chunk pre-fill: kd, vd
-// [B, W, Hkv, D].  Slots no token has reached become zeros, so that the
-// attention's masked products there stay 0.  16 codes per thread and step.
+// [B, W, Hkv, D].  Slots that no query of the chunk sees -- those no token has
+// reached, and of a full buffer the one that holds position start - W -- become
+// zeros, so that the attention's masked products there stay 0 whatever they
+// hold.  16 codes per thread and step: 33 MB read and 67 written at B=2, W=4096
+// in 12 us, beside 180 us of attention for chunks of 1000.
 __global__ void swa_widen_q8_kernel(const uint4 *__restrict__ k_cache, const uint4 *__restrict__ v_cache,
                                     const float *__restrict__ k_scale, const float *__restrict__ v_scale,
                                     const int32_t *__restrict__ pos, uint4 *__restrict__ kd,
@@ -303,7 +306,8 @@ __global__ void swa_widen_q8_kernel(const uint4 *__restrict__ k_cache, const uin
         const int c = (int)(i % row_vec);
         const long long bs = i / row_vec;
         const int slot = (int)(bs % W), b = (int)(bs / W);
-        const bool there = slot < __ldg(pos + b);
+        const int p = __ldg(pos + b);
+        const bool there = slot < p && (p < W || slot != p % W);
         const size_t si = ((size_t)b * nblk + slot / block) * Hkv + c / head_vec;
         if (!in_bounds(b, B) || !in_bounds(slot / block, nblk)) continue;
 #pragma unroll

@@ -1011,7 +1011,8 @@ swa_status_t prefill_weights_sizes(int B, int T, int N, int Hq, int Hkv, int D, 
     if (swa_status_t e = check_heads(Hq, Hkv, D)) return e;
     if (Hq / Hkv > 128) return SWA_ERR_UNSUPPORTED;          // a query tile holds a position's whole group
     const WeightsLayout l = weights_layout(B, T, N, Hq, Hkv, W);
-    if (l.units1 > 0x7fffffffll || l.units2 > 0x7fffffffll) return SWA_ERR_UNSUPPORTED;
+    if (l.units1 > 0x7fffffffll || l.units2 > 0x7fffffffll || (long long)B * Hkv * l.nqt > 0x7fffffffll)
+        return SWA_ERR_UNSUPPORTED;
     return SWA_OK;
 }
 
