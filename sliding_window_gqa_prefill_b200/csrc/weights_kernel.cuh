@@ -24,11 +24,18 @@
 // products of each stationary tile; a warpgroup reads its 64 columns in two
 // loads and gives the product back halfway through, so the tensor core is up to
 // a step and a half ahead.  (One product per warpgroup, given back at three
-// quarters, left it waiting: both measured 690 to 700 us at T = N = 8192, 32 / 8 heads.)
+// quarters, is as fast; the stationary tiles as the products' operand in tensor
+// memory, three products beside them, slower: 738 against 683 us.)
 //
-// What bounds it: one exponential per score and pass, 16 per clock and SM on
-// the special-function unit: 1024 clocks for a 128 x 128 product whose MMA takes
-// 512.  kWeightsPoly pairs in 16 therefore go to a polynomial on the FMA pipe.
+// What bounds it: one exponential per score and pass, 16 per clock and SM on the
+// special-function unit: 1024 clocks for a 128 x 128 product whose MMA takes 512.
+// kWeightsPoly of 16 pairs therefore go to a polynomial on the FMA pipe (none
+// 726, 4 of 16 698, 5 720, 8 798 us).  T = N = 8192, 32 / 8 heads, D=128, both
+// passes: 683 us, 0.40 PFLOP/s of one pass's products.  At 1.55 GHz a product
+// takes 1200 clocks, in which the schedulers issue 62% of the time and no pipe is
+// above 57% busy: 6.9 instructions per score against the 4.4 of its arithmetic,
+// the rest barriers, masks and loads per 64 columns; without the exponentials it
+// still takes 880.  T = 64 of N = 16384, two sequences: 57 us.
 #pragma once
 
 #include "weights_plan.cuh"
@@ -67,10 +74,10 @@ __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
 
-// The largest of three, NaN ignored as by fmaxf.
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
+// The largest of three; a NaN among them stays one.
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
     float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
 
@@ -322,49 +329,60 @@ swa_prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar_s_empty + 8 * d);
                     }
+                    int lo = 0, hi = 32;                     // columns of these 32 that the row sees
                     if (masked) {
                         const WeightsMask M = weights_mask<ROW_IS_QUERY>(p, U, Q_STAYS ? U.a + i : tile,
                                                                          Q_STAYS ? tile : U.a + i, row, row_pos);
-                        const int lo = M.lo - half * 64 - c * 32, hi = M.hi - half * 64 - c * 32;
+                        lo = M.lo - half * 64 - c * 32;
+                        hi = M.hi - half * 64 - c * 32;
+                        if (ROW_IS_QUERY) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (e < lo || e >= hi) x[e] = 0xFF800000u;                            // -inf
+                            for (int e = 0; e < 32; ++e)
+                                if (e < lo || e >= hi) x[e] = 0xFF800000u;                        // -inf
+                        }
                     }
                     float2 off = make_float2(0.f, 0.f);
                     if (ROW_IS_QUERY) {
                         float mx[2] = {__uint_as_float(x[0]), __uint_as_float(x[1])};
 #pragma unroll
                         for (int e = 2; e < 30; e += 4) {
-                            mx[0] = fmax3(mx[0], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-                            mx[1] = fmax3(mx[1], __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+                            mx[0] = fmax3_nan(mx[0], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                            mx[1] = fmax3_nan(mx[1], __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
                         }
-                        mx[0] = fmax3(mx[0], __uint_as_float(x[30]), __uint_as_float(x[31]));
-                        const float mt = fmaxf(mx[0], mx[1]) * sl2.x;
+                        mx[0] = fmax3_nan(mx[0], __uint_as_float(x[30]), __uint_as_float(x[31]));
+                        const float mt = fmax3_nan(mx[0], mx[1], mx[1]) * sl2.x;
                         // the offset is raised when a score exceeds it by more than
-                        // 2^8: the sum keeps its 24 bits either way
-                        if (mt > m + 8.0f) {
+                        // 2^8: the sum keeps its 24 bits either way.  A NaN (which the
+                        // polynomial would not show) makes offset and sum NaN for good.
+                        if (!(mt <= m + 8.0f)) {
                             l *= ex2_approx(m - mt);
                             m = mt;
                         }
                         off.x = off.y = m == -INFINITY ? 0.f : -m;
                     }
                     float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                    // 2^-inf of a masked score is to be 0 exactly: not the polynomial
-                    auto add = [&](uint32_t poly) {
+                    // 2^-inf of a masked score is to be 0 exactly: not the polynomial;
+                    // where the rows are keys the exponent is masked, as the -lse of a
+                    // query that is not finite is +infinity
+                    auto add = [&](uint32_t poly, bool mask) {
                         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             if (!ROW_IS_QUERY && e % 2 == 0) v = lds_f32x4(lse_s + c * 128 + e * 8);     // -lse
                             const float2 o = ROW_IS_QUERY ? off : e % 2 ? make_float2(v.z, v.w) : make_float2(v.x, v.y);
-                            const float2 y = ffma2(
+                            float2 y = ffma2(
                                 make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sl2, o);
+                            if (!ROW_IS_QUERY && mask) {
+                                if (2 * e < lo || 2 * e >= hi) y.x = -INFINITY;
+                                if (2 * e + 1 < lo || 2 * e + 1 >= hi) y.y = -INFINITY;
+                            }
                             acc[e & 1] = fadd2(acc[e & 1], ((poly >> e) & 1u)
                                                                ? exp2_poly2_fine(y)
                                                                : make_float2(ex2_approx(y.x), ex2_approx(y.y)));
                         }
                     };
-                    if (masked) add(0u);
-                    else add(kWeightsPoly);
+                    if (masked) add(0u, true);
+                    else add(kWeightsPoly, false);
                     const float2 sum = fadd2(acc[0], acc[1]);
                     l += sum.x + sum.y;
                 }
@@ -409,7 +427,9 @@ swa_prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
 }
 
 // Joins the lse pass's partial {max, sum} of each row: -lse, or -infinity for a
-// row that is no query (so that its weights are 2^-inf = 0).
+// row that is no query (so that its weights are 2^-inf = 0).  A query whose
+// scores are not finite gets +infinity, with which every weight it gives is not
+// finite either, by whichever exponential (the polynomial would hide a NaN).
 __global__ void __launch_bounds__(128)
 swa_weights_lse_kernel(const float2 *__restrict__ ml, float *__restrict__ lse, const int32_t *__restrict__ lens, int N,
                        int T, int Hkv, int G, int TQ, int nqt, int parts) {
@@ -430,6 +450,7 @@ swa_weights_lse_kernel(const float2 *__restrict__ ml, float *__restrict__ lse, c
         for (int i = 0; i < parts; ++i) m = fmaxf(m, src[i].x);
         for (int i = 0; i < parts; ++i) l += src[i].x == -INFINITY ? src[i].y : src[i].y * ex2_approx(src[i].x - m);
         out = -((m == -INFINITY ? 0.f : m) + __log2f(l));
+        if (!(fabsf(out) < INFINITY)) out = INFINITY;
     }
     lse[row] = out;
 }

@@ -118,6 +118,26 @@ def test_every_query_gives_one_unit_of_weight():
     assert (total - torch.tensor([[2100.0], [1500.0]], device="cuda")).abs().max() < 2100 * 2.0 ** -16
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_what_is_not_finite_shows_where_it_is_seen(value):
+    """A key (or query) that is not finite makes the weights of the queries that
+    see it, and so of the keys they see, not finite; other sequences and heads
+    keep theirs."""
+    rng = np.random.default_rng(9)
+    for where in range(40, 56):                        # every column pair of the exponentials
+        q, k = rows(rng, 2, 200, 2, 64), rows(rng, 2, 200, 2, 64)
+        q[..., 5] = q[..., 5].abs() + 0.1              # an infinite key scores +infinity
+        clean = swa.swa_prefill_weights(q, k, i32([200, 200]), 200, 0.1)
+        k[0, where, 0, 5] = value
+        w = swa.swa_prefill_weights(q, k, i32([200, 200]), 200, 0.1)
+        assert not torch.isfinite(w[0, 0]).any()       # query 199 sees all of them
+        assert torch.equal(w[1], clean[1]) and torch.equal(w[0, 1], clean[0, 1])
+    q, k = rows(rng, 1, 200, 1, 64), rows(rng, 1, 200, 1, 64)
+    q[0, 150, 0, 3] = value
+    w = swa.swa_prefill_weights(q, k, i32([200]), 200, 0.1)
+    assert not torch.isfinite(w[0, 0, :151]).any() and torch.isfinite(w[0, 0, 151:]).all()
+
+
 def test_a_length_outside_the_prompt_gives_zeros_and_is_recorded():
     rng = np.random.default_rng(5)
     run(rng, 3, 140, 9, 4, 2, 64, 140, [141, -1, 140])
