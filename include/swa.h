@@ -432,7 +432,7 @@ size_t swa_prefill_weights_workspace_size(int B, int T, int N, int Hq, int Hkv, 
  * others, the M - S - R of largest weight (ties: the lowest position; NaN
  * counts as infinity), in the order of their positions.  weights_out [B, Hkv,
  * M] receives the kept weights.  Unused slots get slot_pos -1 and weight 0;
- * their K and V are left as they were.  A length outside [0, N] is recorded as
+ * their K and V are left as they were.  The outputs must not overlap the inputs.  A length outside [0, N] is recorded as
  * SWA_ERR_INVALID_ARG and keeps nothing. */
 swa_status_t swa_cache_keep(const void *k, const void *v, const float *weights, const int32_t *lens,
                             void *k_cache, void *v_cache, int32_t *slot_pos, float *weights_out, int B,

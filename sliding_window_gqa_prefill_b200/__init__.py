@@ -539,7 +539,7 @@ def swa_decode_q8(q, k_cache, v_cache, k_scale, v_scale, pos, scale: float, bloc
         out = _empty(q, rows, torch.bfloat16, stream)
     L = lib()
     workspace, ws, size = _scratch(workspace, L.swa_decode_q8_workspace_size(B, Hq, Hkv, D, W), q, dev, stream)
-    _check(L.swa_decode_q8(*args, _ptr(out, "out", torch.bfloat16, rows, dev), B, Hq, Hkv, D, W, block, scale, ws, size,
+    _check(L.swa_decode_q8(*args, _ptr(out, "out", torch.bfloat16, rows, dev), B, Hq, Hkv, D, W, block, float(scale), ws, size,
                            _stream(stream, dev)), "swa_decode_q8")
     return out
 
@@ -570,8 +570,8 @@ def swa_prefill_chunk_q8(q, k, v, k_cache, v_cache, k_scale, v_scale, start_pos,
         out = _empty(q, rows, torch.bfloat16, stream)
     L = lib()
     workspace, ws, size = _scratch(workspace, L.swa_prefill_chunk_q8_workspace_size(B, Hkv, D, W), q, dev, stream)
-    _check(L.swa_prefill_chunk_q8(*args, _ptr(out, "out", torch.bfloat16, rows, dev), B, C, Hq, Hkv, D, W, block, scale,
-                                  ws, size, _stream(stream, dev)), "swa_prefill_chunk_q8")
+    _check(L.swa_prefill_chunk_q8(*args, _ptr(out, "out", torch.bfloat16, rows, dev), B, C, Hq, Hkv, D, W, block,
+                                  float(scale), ws, size, _stream(stream, dev)), "swa_prefill_chunk_q8")
     return out
 
 
@@ -596,8 +596,8 @@ def swa_cache_evict_append(k_new, v_new, k_cache, v_cache, slot_pos, weights, po
             _ptr(pos, "pos", torch.int32, (B,), dev))
     if slots is None:
         slots = _empty(k_cache, (B, Hkv), torch.int32, stream)
-    _check(lib().swa_cache_evict_append(*args, _ptr(slots, "slots", torch.int32, (B, Hkv), dev), B, Hkv, D, M, S, R,
-                                        _stream(stream, dev)), "swa_cache_evict_append")
+    _check(lib().swa_cache_evict_append(*args, _ptr(slots, "slots", torch.int32, (B, Hkv), dev), B, Hkv, D, M, int(S),
+                                        int(R), _stream(stream, dev)), "swa_cache_evict_append")
     return slots
 
 
@@ -631,7 +631,7 @@ def swa_decode_weights(q, k_cache, v_cache, slot_pos, weights, pos, scale: float
     workspace, ws, size = _scratch(workspace, L.swa_decode_weights_workspace_size(B, Hq, Hkv, D, M), q, dev, stream)
     _check(L.swa_decode_weights(*args, _ptr(weights_out, "weights_out", f32, state, dev),
                                 _ptr(pos, "pos", torch.int32, (B,), dev), _ptr(out, "out", bf16, rows, dev), B, Hq, Hkv,
-                                D, M, scale, ws, size, _stream(stream, dev)), "swa_decode_weights")
+                                D, M, float(scale), ws, size, _stream(stream, dev)), "swa_decode_weights")
     return out, weights_out
 
 
@@ -653,10 +653,10 @@ def swa_prefill_weights(q, k, lens, W: int, scale: float, weights=None, workspac
     if weights is None:
         weights = _empty(q, (B, Hkv, N), torch.float32, stream)
     L = lib()
-    W = min(W, N)
+    W = min(int(W), N)
     workspace, ws, size = _scratch(workspace, L.swa_prefill_weights_workspace_size(B, T, N, Hq, Hkv, D, W), q, dev, stream)
     _check(L.swa_prefill_weights(*args, _ptr(weights, "weights", torch.float32, (B, Hkv, N), dev), B, T, N, Hq, Hkv, D,
-                                 W, scale, ws, size, _stream(stream, dev)), "swa_prefill_weights")
+                                 W, float(scale), ws, size, _stream(stream, dev)), "swa_prefill_weights")
     return weights
 
 
@@ -678,4 +678,4 @@ def swa_cache_keep(k, v, weights, lens, k_cache, v_cache, slot_pos, weights_out,
         _ptr(weights, "weights", f32, (B, Hkv, N), dev), _ptr(lens, "lens", torch.int32, (B,), dev),
         _ptr(k_cache, "k_cache", bf16, dims, dev), _ptr(v_cache, "v_cache", bf16, dims, dev),
         _ptr(slot_pos, "slot_pos", torch.int32, state, dev), _ptr(weights_out, "weights_out", f32, state, dev),
-        B, N, Hkv, D, M, S, R, _stream(stream, dev)), "swa_cache_keep")
+        B, N, Hkv, D, M, int(S), int(R), _stream(stream, dev)), "swa_cache_keep")

@@ -356,7 +356,9 @@ __global__ void swa_widen_q8_kernel(const uint4 *__restrict__ k_cache, const uin
 // 16-byte shared load per row and half, V by one per key, and the bytes of two
 // keys are paired by byte permutes.
 //
-// Measured at B=64, W=4096, 32 / 8 heads, D=128: 99 to 101 us, 5.4 TB/s.  With
+// Measured at B=64, W=4096, 32 / 8 heads, D=128: 88 us, 6.1 TB/s.  With four
+// splits to a window instead of one (3.46 rounds of blocks instead of less than
+// one, and their merge) 99 to 101 us, and the following on top of that: with
 // both products in f16 and the heads as rows of both it took 114 to 142 us (the
 // 16-bit copies of K cost registers, and the O product half its rows); with K
 // alone in f16 104 us.  Four blocks of four warps to an SM, 3 stages of 16 keys:

@@ -668,12 +668,60 @@ swa_status_t append_q8_impl(const void *k_new, const void *v_new, void *k_cache,
 #undef SWA_APPEND_Q8
 }
 
+// Keys per split of an 8-bit decode over L keys by `pairs` (sequence, group of
+// heads) pairs: the number of splits with the least estimated time, in the time
+// a block takes per key: the rounds of blocks (592 run at once, 4 to an SM) times
+// the keys of one and kQ8BlockCost for its start and its merge, and, unless
+// there is one split or four (which merge in their cluster), kQ8MergeCost and
+// kQ8MergePart per split for the merge kernel.  Splits are multiples of 64 keys,
+// at least kDecodeMinSplit.  Against the 16-bit decode's rule (up to 1024 keys):
+// B=64, W=4096, 8 KV heads, one split instead of four 88 against 101 us, W=2000
+// one instead of two 49 against 58; small batches are cut alike.  A function of
+// the sizes only: the workspace size follows from it.
+constexpr int kQ8BlocksAtOnce = 592, kQ8BlockCost = 200, kQ8MergeCost = 60, kQ8MergePart = 37;
+
+int q8_split_keys(int B, int Hkv, int L) {
+    const long long pairs = (long long)B * Hkv;
+    long long best = 0;
+    int split = 0;
+    for (int n = 1; n <= 64; ++n) {
+        const long long s = (((long long)L + n - 1) / n + 63) / 64 * 64;
+        if (n > 1 && s < swa::kDecodeMinSplit) break;
+        const long long rounds = (pairs * n + kQ8BlocksAtOnce - 1) / kQ8BlocksAtOnce;
+        const long long cost = rounds * (s + kQ8BlockCost) +
+                               (n == 1 || n == swa::kDecodeClusterSplits ? 0 : kQ8MergeCost + n * kQ8MergePart);
+        if (split == 0 || cost < best) {
+            best = cost;
+            split = (int)(s < 0x7fffffc0ll ? s : 0x7fffffc0ll);
+        }
+    }
+    return split;
+}
+
+int q8_nsplit(int B, int Hkv, int L) {
+    const int split = q8_split_keys(B, Hkv, L);
+    return (int)(((long long)L + split - 1) / split);
+}
+
+// 0 where the window is one split or the splits are merged on chip (or the
+// sizes are invalid).
+size_t decode_q8_workspace_bytes(int B, int Hq, int Hkv, int D, int W) {
+    if (B < 1 || W < 1 || check_heads(Hq, Hkv, D) != SWA_OK) return 0;
+    int rep = 1;
+    decode_group(Hq, Hkv, &rep);
+    if ((long long)Hkv * rep > 65535) return 0;
+    const int nsm = q8_nsplit(B, Hkv * rep, W);
+    if (nsm == 1 || nsm == swa::kDecodeClusterSplits) return 0;
+    const size_t rows = (size_t)B * Hq * nsm;
+    return ((rows * D * 4 + 255) & ~size_t(255)) + rows * 8;
+}
+
 template <int D, int G>
 swa_status_t launch_decode_q8_dg(const void *q, const void *kc, const void *vc, const float *ks, const float *vs,
                                  const int32_t *pos, void *out, int B, int Hkv, int W, int block, float scale,
                                  void *ws, int kv_rep, cudaStream_t s) {
-    const int nsm = decode_nsplit_max(B, Hkv, W);
-    const int split = decode_split_keys(B, Hkv, W);
+    const int nsm = q8_nsplit(B, Hkv, W);
+    const int split = q8_split_keys(B, Hkv, W);
     const bool cluster = nsm == swa::kDecodeClusterSplits;
     const size_t o_elems = (size_t)B * Hkv * nsm * G * D;
     float *ws_o = static_cast<float *>(ws);
@@ -731,17 +779,6 @@ swa_status_t launch_decode_q8_dg(const void *q, const void *kc, const void *vc, 
         case 16: return LAUNCH<128, 8>(__VA_ARGS__);                            \
         default: return SWA_ERR_UNSUPPORTED;                                    \
     }
-
-// That of decode, or 0 where the window is one split or the splits are merged on
-// chip (or the sizes are invalid).
-size_t decode_q8_workspace_bytes(int B, int Hq, int Hkv, int D, int W) {
-    const size_t bytes = decode_workspace_bytes(B, Hq, Hkv, D, W);
-    if (bytes == 0) return 0;
-    int rep = 1;
-    decode_group(Hq, Hkv, &rep);
-    const int nsm = decode_nsplit_max(B, Hkv * rep, W);
-    return nsm == 1 || nsm == swa::kDecodeClusterSplits ? 0 : bytes;
-}
 
 swa_status_t decode_q8_impl(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
                             const float *v_scale, const int32_t *pos, void *out, int B, int Hq, int Hkv, int D,

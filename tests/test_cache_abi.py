@@ -41,14 +41,15 @@ def test_append_q8(lib):
 
 def test_decode_q8(lib):
     #        q  kc vc ks vs pos out B  Hq Hkv D  W  block scale ws bytes stream
-    good = [P] * 7 + [1, 4, 2, 64, 600, 16, 0.1, P, 1 << 30, None]
+    good = [P] * 7 + [1, 4, 2, 64, 6000, 16, 0.1, P, 1 << 30, None]
     vary(lib.swa_decode_q8, good, pointers(7) + [
         ({7: 0}, BAD), ({8: 3}, BAD), ({9: 0}, BAD), ({10: 96}, UNSUP), ({11: 0}, BAD), ({12: 24}, BAD),
         ({13: 0.0}, BAD), ({13: float("nan")}, BAD), ({13: float("inf")}, BAD), ({14: None}, BAD), ({14: P + 128}, BAD),
         ({15: 16}, BAD), ({7: 65536}, UNSUP)])
     size = lib.swa_decode_q8_workspace_size
     assert size(1, 4, 2, 64, 600) >= 3 * 4 * 64 * 4                       # 3 splits
-    assert size(1, 4, 2, 64, 200) == size(64, 32, 8, 128, 4096) == 0      # one split; merged in the cluster
+    assert size(1, 4, 2, 64, 200) == size(64, 32, 8, 128, 4096) == 0      # one split
+    assert size(2, 4, 2, 64, 1000) == 0                                   # four, merged in their cluster
     assert size(1, 3, 2, 64, 600) == size(0, 4, 2, 64, 600) == size(1, 4, 2, 72, 600) == 0
 
 

@@ -226,10 +226,11 @@ def test_decode_windows(block, W):
     decode_and_check(rng, 5, 4, 2, 64, W, block, [0, W // 2, W - 1, W, 3 * W + 1])
 
 
-@pytest.mark.parametrize("B,H,W", [(2, 2, 1024), (1, 1, 1111), (8, 8, 4096), (1, 1, 9000)])
+@pytest.mark.parametrize("B,H,W", [(2, 2, 1024), (1, 1, 1111), (8, 8, 4096), (1, 1, 9000), (1, 1, 40000), (74, 8, 300),
+                                   (40, 4, 900)])
 def test_decode_splits(B, H, W):
-    """Windows of 4 splits (merged in a cluster), of 5, of the batch's 4 splits of
-    1024 keys, and of more splits than the merge unrolls."""
+    """Windows of 4 splits (merged in a cluster), of 8 and 16, of more than the
+    merge unrolls, of one split each, and of 3."""
     rng = np.random.default_rng(W)
     decode_and_check(rng, B, 4 * H, H, 128, W, 64, [W * 2 + 5 if b % 2 == 0 else (W * b) // B for b in range(B)])
 
