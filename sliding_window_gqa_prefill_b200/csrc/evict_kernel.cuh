@@ -685,23 +685,31 @@ swa_keep_select_kernel(const float *__restrict__ weights, const int32_t *__restr
 }
 
 // Copies the kept rows: slot s of KV head g from row slot_pos[b, g, s] of the
-// prompt; free slots stay as they are.  16 bytes of K and of V per thread.
-__global__ void swa_keep_copy_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v,
-                                     const int32_t *__restrict__ slot_pos, uint4 *__restrict__ k_cache,
-                                     uint4 *__restrict__ v_cache, int B, int N, int Hkv, int M, int head_vec) {
-    const long long total = (long long)B * M * Hkv * head_vec;
-    for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < total;
-         i += (long long)gridDim.x * blockDim.x) {
-        const int c = (int)(i % head_vec);
-        const long long bsg = i / head_vec;
-        const int g = (int)(bsg % Hkv);
-        const long long bs = bsg / Hkv;
-        const int s = (int)(bs % M), b = (int)(bs / M);
-        const int j = __ldg(slot_pos + ((size_t)b * Hkv + g) * M + s);
+// prompt; free slots stay as they are.  16 bytes of K and of V per thread and
+// step; grid y the sequence, x strides over its vectors, slot and vector of the
+// row carried along.
+__global__ void __launch_bounds__(256)
+swa_keep_copy_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v, const int32_t *__restrict__ slot_pos,
+                     uint4 *__restrict__ k_cache, uint4 *__restrict__ v_cache, int N, int Hkv, int M, int head_vec) {
+    const int row_vec = Hkv * head_vec;
+    const int b = blockIdx.y;
+    const size_t to = (size_t)b * M * row_vec, from = (size_t)b * N * row_vec;
+    const int32_t *at = slot_pos + (size_t)b * Hkv * M;
+    const long long first = blockIdx.x * (long long)blockDim.x + threadIdx.x, step = (long long)gridDim.x * blockDim.x;
+    int c = (int)(first % row_vec);
+    long long s = first / row_vec;
+    const int step_c = (int)(step % row_vec);
+    const long long step_s = step / row_vec;
+    for (; s < M; s += step_s, c += step_c) {
+        if (c >= row_vec) {
+            c -= row_vec;
+            if (++s >= M) break;
+        }
+        const int j = __ldg(at + (size_t)(c / head_vec) * M + s);
         if (j < 0 || !in_bounds(j, N)) continue;
-        const size_t src = (((size_t)b * N + j) * Hkv + g) * head_vec + c;
-        k_cache[i] = __ldg(k + src);
-        v_cache[i] = __ldg(v + src);
+        const size_t src = from + (size_t)j * row_vec + c, dst = to + (size_t)s * row_vec + c;
+        k_cache[dst] = __ldg(k + src);
+        v_cache[dst] = __ldg(v + src);
     }
 }
 

@@ -617,6 +617,15 @@ swa_status_t decode_impl(const void *q, const void *k_cache, const void *v_cache
 // ----------------------------------------------------------------- 8-bit rolling cache
 bool misaligned(const void *p, uintptr_t by) { return (reinterpret_cast<uintptr_t>(p) & (by - 1)) != 0; }
 
+// Grid of a copy kernel of 256 threads over `vectors` per sequence: about 16
+// blocks to an SM in all.
+dim3 copy_grid(long long vectors, int B, int sms) {
+    long long x = (vectors + 255) / 256;
+    const long long most = ((long long)sms * 16 + B - 1) / B;
+    if (x > most) x = most;
+    return dim3((unsigned)(x < 1 ? 1 : x), B);
+}
+
 // Slots per scale: a power of two that the decode kernel's 16-key blocks divide.
 bool bad_q8_block(int block) { return block != 16 && block != 32 && block != 64 && block != 128; }
 
@@ -818,11 +827,9 @@ swa_status_t prefill_chunk_q8_impl(const void *q, const void *k, const void *v, 
     const size_t half = (size_t)B * W * Hkv * D * 2;
     char *kd = static_cast<char *>(workspace), *vd = kd + half;
     const int nblk = (int)(((long long)W + block - 1) / block);
-    long long blocks = ((long long)B * W * Hkv * (D / 16) + 255) / 256;
-    if (blocks > (long long)dev->sms * 16) blocks = (long long)dev->sms * 16;
-    swa::swa_widen_q8_kernel<<<(int)blocks, 256, 0, s>>>(
+    swa::swa_widen_q8_kernel<<<copy_grid((long long)W * Hkv * (D / 16), B, dev->sms), 256, 0, s>>>(
         static_cast<const uint4 *>(k_cache), static_cast<const uint4 *>(v_cache), k_scale, v_scale, start_pos,
-        reinterpret_cast<uint4 *>(kd), reinterpret_cast<uint4 *>(vd), B, W, Hkv, D / 16, block, nblk);
+        reinterpret_cast<uint4 *>(kd), reinterpret_cast<uint4 *>(vd), W, Hkv, D / 16, block, nblk);
     SWA_CUDA_TRY(cudaGetLastError());
     if (swa_status_t e = prefill_chunk_impl(q, k, v, kd, vd, start_pos, out, B, C, Hq, Hkv, D, W, scale, nullptr,
                                             nullptr, s, nullptr, nullptr, 0, false))
@@ -988,11 +995,9 @@ swa_status_t keep_impl(const void *k, const void *v, const float *weights, const
     swa::swa_keep_select_kernel<<<dim3(Hkv, B), swa::kKeepThreads, swa::keep_smem(N), s>>>(
         weights, lens, slot_pos, weights_out, N, Hkv, M, S, R);
     SWA_CUDA_TRY(cudaGetLastError());
-    long long blocks = ((long long)B * M * Hkv * (D / 8) + 255) / 256;
-    if (blocks > (long long)dev->sms * 16) blocks = (long long)dev->sms * 16;
-    swa::swa_keep_copy_kernel<<<(int)blocks, 256, 0, s>>>(
+    swa::swa_keep_copy_kernel<<<copy_grid((long long)M * Hkv * (D / 8), B, dev->sms), 256, 0, s>>>(
         static_cast<const uint4 *>(k), static_cast<const uint4 *>(v), slot_pos, static_cast<uint4 *>(k_cache),
-        static_cast<uint4 *>(v_cache), B, N, Hkv, M, D / 8);
+        static_cast<uint4 *>(v_cache), N, Hkv, M, D / 8);
     SWA_CUDA_TRY(cudaGetLastError());
     return SWA_OK;
 }
