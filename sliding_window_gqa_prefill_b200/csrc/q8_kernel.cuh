@@ -365,7 +365,9 @@ swa_widen_q8_kernel(const uint4 *__restrict__ k_cache, const uint4 *__restrict__
 // 16-byte shared load per row and half, V by one per key, and the bytes of two
 // keys are paired by byte permutes.
 //
-// Measured at B=64, W=4096, 32 / 8 heads, D=128: 88 us, 6.1 TB/s.  With four
+// Measured at B=64, W=4096, 32 / 8 heads, D=128: 88 us, 6.1 TB/s (100 to 104 in
+// loops of a tenth of a second and more, where the power cap lowers the clock:
+// the ALU is half busy with the conversions).  With four
 // splits to a window instead of one (3.46 rounds of blocks instead of less than
 // one, and their merge) 99 to 101 us, and the following on top of that: with
 // both products in f16 and the heads as rows of both it took 114 to 142 us (the
@@ -577,8 +579,10 @@ swa_decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         for (int h = 0; h < HALVES; ++h) {
             const int blk = min(stage0 + 16 * h, end - 1) >> block_log2;
             if (!in_bounds(blk, nblk)) continue;
-            ks[h] = __ldg(ksb + (size_t)blk * Hkv_mem);
-            vs[h] = __ldg(vsb + (size_t)blk * Hkv_mem);
+            // below 2^32: more scales would stand for over 4 TB of codes
+            const uint32_t at = (uint32_t)blk * (uint32_t)Hkv_mem;
+            ks[h] = __ldg(ksb + at);
+            vs[h] = __ldg(vsb + at);
         }
     };
     int stage0 = begin + warp * kQ8Stage;
@@ -628,7 +632,7 @@ swa_decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                     if (key0 + 2 * t4 + (e & 1) + (e >> 1) * 8 >= end) sc[e] = -INFINITY;
             }
             float mx = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
-            if (__any_sync(0xffffffffu, head_ok && mx > m_run + 8.0f)) {
+            if (__any_sync(0xffffffffu, mx > m_run + 8.0f)) {
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 float alpha = 1.f;
@@ -651,7 +655,7 @@ swa_decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             const float off = 7.0f - m_run;
             float pw[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) pw[e] = head_ok ? ex2_approx(sc[e] + off) : 0.f;
+            for (int e = 0; e < 4; ++e) pw[e] = ex2_approx(sc[e] + off);   // of rows past G too: never read
             const uint32_t pb0 = pack_f16x2(pw[0], pw[1]), pb1 = pack_f16x2(pw[2], pw[3]);
             {
                 const float2 l0 = f16x2_to_f32x2(pb0), l1 = f16x2_to_f32x2(pb1);
