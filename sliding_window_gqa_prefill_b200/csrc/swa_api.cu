@@ -686,22 +686,25 @@ swa_status_t append_q8_impl(const void *k_new, const void *v_new, void *k_cache,
 // at least kDecodeMinSplit.  Against the 16-bit decode's rule (up to 1024 keys):
 // B=64, W=4096, 8 KV heads, one split instead of four 88 against 101 us, W=2000
 // one instead of two 49 against 58; small batches are cut alike.  A function of
-// the sizes only: the workspace size follows from it.
+// the sizes only: the workspace size follows from it.  (The longest split keeps
+// the kernels' 32-bit sums of a window and a split in range.)
+constexpr long long kQ8MaxSplit = 1 << 24;
 constexpr int kQ8BlocksAtOnce = 592, kQ8BlockCost = 200, kQ8MergeCost = 60, kQ8MergePart = 37;
 
 int q8_split_keys(int B, int Hkv, int L) {
     const long long pairs = (long long)B * Hkv;
     long long best = 0;
-    int split = 0;
-    for (int n = 1; n <= 64; ++n) {
+    int split = (int)kQ8MaxSplit;
+    for (int n = 1; n <= 128; ++n) {
         const long long s = (((long long)L + n - 1) / n + 63) / 64 * 64;
+        if (s > kQ8MaxSplit) continue;
         if (n > 1 && s < swa::kDecodeMinSplit) break;
         const long long rounds = (pairs * n + kQ8BlocksAtOnce - 1) / kQ8BlocksAtOnce;
         const long long cost = rounds * (s + kQ8BlockCost) +
                                (n == 1 || n == swa::kDecodeClusterSplits ? 0 : kQ8MergeCost + n * kQ8MergePart);
-        if (split == 0 || cost < best) {
+        if (best == 0 || cost < best) {
             best = cost;
-            split = (int)(s < 0x7fffffc0ll ? s : 0x7fffffc0ll);
+            split = (int)s;
         }
     }
     return split;
