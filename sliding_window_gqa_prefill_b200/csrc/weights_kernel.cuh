@@ -87,6 +87,12 @@ __device__ __forceinline__ float4 lds_f32x4(uint32_t a) {
     return v;
 }
 
+__device__ __forceinline__ float2 lds_f32x2(uint32_t a) {
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+    return v;
+}
+
 // 2^x for two values on the FMA pipe, as exp2_poly2 but to the accuracy of the
 // special-function unit: degree 5, fitted in the same way (relative error
 // 1.3e-7 in fp32).  x is clamped at -126.
@@ -312,8 +318,15 @@ swa_prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
                 }
                 tc_fence_after();
                 const int tile = U.first + j;
-                const bool masked = tile < clear.lo || tile > clear.hi;
                 const uint32_t lse_s = sbase + Cfg::OFF_LSE + (MODE == kWeightsByKey ? s : (uint32_t)i) * 512 + half * 256;
+                // a product with a query that is not finite (-lse: +infinity) keeps
+                // off the polynomial too: a score that is NaN, or -infinity, makes
+                // the exponent NaN, which the polynomial's clamp would hide
+                bool masked = tile < clear.lo || tile > clear.hi;
+                if (!ROW_IS_QUERY) {
+                    const float2 v = lds_f32x2(lse_s + lane * 8);
+                    masked |= __any_sync(0xffffffffu, fmaxf(v.x, v.y) == INFINITY);
+                }
                 const uint32_t tD = tS + 256 * ((cnt + j) & 1);
                 uint32_t r[2][32];
                 tmem_ld32(tD, r[0]);
@@ -427,9 +440,10 @@ swa_prefill_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
 }
 
 // Joins the lse pass's partial {max, sum} of each row: -lse, or -infinity for a
-// row that is no query (so that its weights are 2^-inf = 0).  A query whose
-// scores are not finite gets +infinity, with which every weight it gives is not
-// finite either, by whichever exponential (the polynomial would hide a NaN).
+// row that is no query (so that it gives 2^-inf = 0, or the polynomial's least,
+// 2^-126).  A query whose scores are not finite gets +infinity, with which every
+// weight it gives is not finite either: the weights pass takes no polynomial
+// beside it.
 __global__ void __launch_bounds__(128)
 swa_weights_lse_kernel(const float2 *__restrict__ ml, float *__restrict__ lse, const int32_t *__restrict__ lens, int N,
                        int T, int Hkv, int G, int TQ, int nqt, int parts) {
@@ -449,7 +463,8 @@ swa_weights_lse_kernel(const float2 *__restrict__ ml, float *__restrict__ lse, c
         float m = -INFINITY, l = 0.f;
         for (int i = 0; i < parts; ++i) m = fmaxf(m, src[i].x);
         for (int i = 0; i < parts; ++i) l += src[i].x == -INFINITY ? src[i].y : src[i].y * ex2_approx(src[i].x - m);
-        out = -((m == -INFINITY ? 0.f : m) + __log2f(l));
+        out = -(m + __log2f(l));
+        // (a query sees its own key at least: no maximum means that all scores are -infinity)
         if (!(fabsf(out) < INFINITY)) out = INFINITY;
     }
     lse[row] = out;
