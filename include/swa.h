@@ -351,7 +351,8 @@ size_t swa_decode_q8_workspace_size(int B, int Hq, int Hkv, int D, int W);
  * them, and causally to the chunk's own 16-bit keys and values; then the chunk
  * is appended as by swa_cache_append_q8.  Requires C <= W.  (As in
  * swa_prefill_chunk, a value row that is not finite also reaches the queries
- * beside those that see it, within their 128-row block.)  workspace: at least
+ * beside those that see it, within their 128-row block, and values above 2^119
+ * / W may overflow the 32-bit sums.)  workspace: at least
  * swa_prefill_chunk_q8_workspace_size() bytes, 256-byte aligned; it holds the
  * window widened to bf16 (exactly) during the call. */
 swa_status_t swa_prefill_chunk_q8(const void *q, const void *k, const void *v, void *k_cache,

@@ -380,6 +380,11 @@ swa_widen_q8_kernel(const uint4 *__restrict__ k_cache, const uint4 *__restrict__
 // handful of instructions.
 constexpr int kQ8Stage = 16;           // keys per TMA box
 constexpr int kQ8Warps = 4;
+// O sums up to 2^24 keys of P up to 2^15 times 448 V scales: below 2^108 for
+// scales up to 2^60.  From the first larger one on a warp holds O 2^-60 times, so
+// that scales up to 2^119 stay below 2^107; only beside such values do those
+// below 2^-73 lose bits.
+constexpr float kQ8LargeScale = 1152921504606846976.f, kQ8DownLog2 = 60.f, kQ8Down = 1.f / kQ8LargeScale;
 
 template <int D, int G>
 struct DecodeQ8Cfg {
@@ -571,6 +576,7 @@ swa_decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         const int r = 2 * t4 + (e & 1) + (e >> 1) * 8;
         voff[e] = ring + Cfg::TILE_BYTES + (D == 128 ? q8_off<D>(r, hr) : q8_off<D>(r, hr >> 1) + (hr & 1) * 8);
     }
+    float vfac = 1.f;                               // O is held vfac times
     constexpr int HALVES = kQ8Stage / 16;
     float ks[HALVES], vs[HALVES];
     // one scale per 16 keys, loaded a stage ahead of its use
@@ -595,7 +601,17 @@ swa_decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 #pragma unroll
         for (int h = 0; h < HALVES; ++h) {
             kf[h] = ks[h] * qfac;
-            vs2[h] = make_float2(vs[h], vs[h]);
+            if (vs[h] * vfac > kQ8LargeScale) {      // uniform; at most once
+                vfac = kQ8Down;
+#pragma unroll
+                for (int mt = 0; mt < Cfg::MT; ++mt)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        o[mt][r].x *= kQ8Down;
+                        o[mt][r].y *= kQ8Down;
+                    }
+            }
+            vs2[h] = make_float2(vs[h] * vfac, vs[h] * vfac);
         }
         if (!__all_sync(0xffffffffu, mbar_wait_bounded(bars + slot * 8, phase, abort_flag, limit))) {
             // let what this warp started land before the block goes on
@@ -710,6 +726,10 @@ swa_decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     }
     l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
     l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
+    if (vfac != 1.f) {                              // {m, l, o} and {m + x, 2^-x l, 2^-x o} are the same
+        l_run *= kQ8Down;
+        m_run += kQ8DownLog2;
+    }
 
     __syncthreads();
     float *mg = reinterpret_cast<float *>(smem);    // [warp][G][D+2]
