@@ -394,7 +394,7 @@ swa_status_t swa_cache_evict_append(const void *k_new, const void *v_new, void *
                                     swa_stream_t stream);
 
 /* swa_decode_weights -- swa_decode over the slots 0 .. min(pos[b]+1, M)-1 that
- * are not free (what a free slot holds is never used), and
+ * hold a position from 0 to pos[b] (what the others hold is never used), and
  *   weights_out[b,g,s] = weights[b,g,s] + sum over the group's heads of the
  *                        softmax weight of slot s.
  * weights NULL: from 0; weights_out may be weights.  A KV head that holds no

@@ -608,10 +608,10 @@ def swa_decode_weights_workspace_size(B: int, Hq: int, Hkv: int, D: int, M: int)
 def swa_decode_weights(q, k_cache, v_cache, slot_pos, weights, pos, scale: float, weights_out=None, out=None,
                        workspace=None, stream=None):
     """Decode one token per sequence over the slots of a fixed-size cache
-    [B,M,Hkv,D] that hold a position (slot_pos [B,Hkv,M] int32 >= 0), and add the
-    softmax weight each slot receives to `weights` [B,Hkv,M] float32 (None: from
-    0).  weights_out: where the sums go (default: weights itself, in place).
-    Returns (out [B,Hq,D], weights_out)."""
+    [B,M,Hkv,D] that hold a position from 0 to pos[b] (slot_pos [B,Hkv,M] int32),
+    and add the softmax weight each slot receives to `weights` [B,Hkv,M] float32
+    (None: from 0).  weights_out: where the sums go (default: weights itself, in
+    place).  Returns (out [B,Hq,D], weights_out)."""
     import torch
     dev = torch.cuda.current_device()
     dims = _dims(k_cache, "k_cache", 4)

@@ -21,8 +21,9 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
 
 // ---------------------------------------------------------------------------
 // Decode that keeps the scores.  As swa_decode_kernel over the slots
-// 0 .. min(pos+1, M)-1 that hold a position, and each block also keeps its
-// scores (base 2, scaled; -inf for a free slot), from which the weights follow
+// 0 .. min(pos+1, M)-1 that hold a position up to pos (a sequence that was taken
+// back leaves later ones; here they are as free slots), and each block also keeps
+// its scores (base 2, scaled; -inf for a free slot), from which the weights follow
 // once the softmax sums are known.  What free slots hold never meets the
 // products: their scores are replaced, and in a 16-key block that has one (a
 // branch the whole warp takes) their values are cleared.  slot_pos comes through
@@ -150,14 +151,14 @@ swa_decode_scores_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat1
         }
         const uint32_t sk = ring + stage * SCfg::STAGE_BYTES, sv = sk + Cfg::BLK_BYTES;
         const int rel = (warp + i * kDecodeWarps) * kDecodeBlk;
-        // which of the block's 16 slots hold a token; >> 2 t4: bit 0, 1, 8, 9 are
+        // which of the block's 16 slots hold a token up to p; >> 2 t4: bit 0, 1, 8, 9 are
         // this lane's keys
         uint32_t held;
         {
             int32_t at = -1;
             if (lane < kDecodeBlk && begin + rel + lane < end)
                 asm volatile("ld.shared.s32 %0, [%1];" : "=r"(at) : "r"(sk + Cfg::STAGE_BYTES + 4 * lane) : "memory");
-            held = __ballot_sync(0xffffffffu, at >= 0);
+            held = __ballot_sync(0xffffffffu, (uint32_t)at <= (uint32_t)p);      // p >= 0; -1: free
         }
         const uint32_t bits = held >> (2 * t4);
 
