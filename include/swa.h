@@ -382,12 +382,18 @@ size_t swa_prefill_chunk_q8_workspace_size(int B, int Hkv, int D, int W);
 
 /* swa_cache_evict_append -- store the token at position pos[b], k_new, v_new
  * [B, Hkv, D], in one slot of each KV head: the slot that already holds pos[b],
- * else the lowest free one, else the one of least weight among those whose
- * position q has S <= q <= pos[b] - R (ties: the lowest slot; NaN counts as
- * infinity).  Its slot_pos becomes pos[b], its weight 0.  slots: int32 [B, Hkv],
- * receives the slot taken, or NULL.  If no slot may be evicted nothing is
- * written, slots gets -1 and SWA_ERR_INVALID_ARG is recorded (as for pos[b] <
- * 0); it cannot happen to a cache that only these calls have filled. */
+ * else the lowest free one, else the lowest that holds a position behind pos[b],
+ * else the one of least weight among those whose position q has S <= q <=
+ * pos[b] - R (ties: the lowest slot; NaN counts as infinity).  Its slot_pos
+ * becomes pos[b], its weight 0.  slots: int32 [B, Hkv], receives the slot taken,
+ * or NULL.  If no slot may be evicted nothing is written, slots gets -1 and
+ * SWA_ERR_INVALID_ARG is recorded (as for pos[b] < 0); it cannot happen to a
+ * cache that only these calls have filled.
+ * A sequence is taken back by going on from a lower pos[b]: slots of positions
+ * behind it are not attended to and are reused.  What the rejected tokens evicted
+ * is gone, and the weight their queries gave stays in `weights` (a caller who
+ * minds keeps a copy, or lets swa_decode_weights write to another array until
+ * they are accepted). */
 swa_status_t swa_cache_evict_append(const void *k_new, const void *v_new, void *k_cache, void *v_cache,
                                     int32_t *slot_pos, float *weights, const int32_t *pos,
                                     int32_t *slots, int B, int Hkv, int D, int M, int S, int R,

@@ -1,6 +1,6 @@
 """A fixed-size cache whose sequence is taken back (tokens proposed and then
-rejected): slots of positions behind the sequence's are not attended to and
-receive nothing.
+rejected): slots of positions behind the sequence's are not attended to, receive
+nothing and are taken before anything is evicted.
 
 Bounds as in tests/test_gpu_evict.py."""
 import math
@@ -66,3 +66,43 @@ def test_positions_behind_the_sequence_are_not_seen(B, Hq, H, D, M):
     q, scale = rows(rng, B, Hq, D), 1 / math.sqrt(D)
     out, w = swa.swa_decode_weights(q, kc, vc, i32(at), w0, i32(pos), scale, weights_out=torch.empty_like(w0))
     check_decode(q, kc, vc, i32(at), w0, w, out, pos, scale)
+
+
+def evict(held, w, p, S, R):
+    """The slot that position p takes: its own, else the lowest free one, else the
+    lowest that holds a position behind p, else the one of least weight."""
+    for want in (lambda x: x == p, lambda x: x < 0, lambda x: x > p):
+        for s, x in enumerate(held):
+            if want(x):
+                return s
+    return ref.evict(held, w, p, S, R)
+
+
+@pytest.mark.parametrize("M,S,R,back", [(24, 2, 5, 3), (24, 2, 5, 12), (8, 4, 4, 6), (9, 1, 2, 5), (33, 0, 1, 30)])
+def test_a_run_that_is_taken_back_and_goes_on(M, S, R, back):
+    """Fill and evict, take `back` tokens back, go on: no slot of a rejected token
+    is seen, and each token finds a slot, also where less than `back` slots are
+    within reach of eviction."""
+    rng = np.random.default_rng(M + back)
+    B, Hq, H, D, scale = 2, 4, 2, 64, 0.125
+    kc = torch.zeros(B, M, H, D, dtype=BF16, device="cuda")
+    vc, at = torch.zeros_like(kc), i32(np.full((B, H, M), -1))
+    w = torch.zeros(B, H, M, device="cuda")
+    for p in list(range(2 * M)) + list(range(2 * M - back, 2 * M + 6)):
+        q, k, v = rows(rng, B, Hq, D), rows(rng, B, H, D), rows(rng, B, H, D)
+        want = [[evict(at[b, h].tolist(), w[b, h].cpu().numpy(), p, S, R) for h in range(H)] for b in range(B)]
+        assert min(min(x) for x in want) >= 0
+        assert swa.swa_cache_evict_append(k, v, kc, vc, at, w, i32([p, p]), S, R).tolist() == want, p
+        w0 = w.clone()
+        out, _ = swa.swa_decode_weights(q, kc, vc, at, w, i32([p, p]), scale)
+        check_decode(q, kc, vc, at, w0, w, out, [p, p], scale)
+
+
+def test_order_of_the_choices():
+    rng = np.random.default_rng(3)
+    at = np.array([[[11, 3, -1, 10], [11, 3, 12, 10], [12, 11, 3, 4], [3, 12, 4, 13]]])
+    w = np.array([[[0, 0, 9, 9], [0, 0, 0, 9], [9, 9, 0, 0], [0, 9, 0, 5]]], np.float32)
+    k, c = rows(rng, 1, 4, 64), rows(rng, 1, 4, 4, 64)
+    got = swa.swa_cache_evict_append(k, k, c, c.clone(), i32(at), torch.tensor(w, device="cuda"), i32([10]), 0, 2)
+    # its own slot, its own slot, the lowest behind it, the lowest behind it (weights do not matter)
+    assert got.tolist() == [[3, 3, 0, 1]]
