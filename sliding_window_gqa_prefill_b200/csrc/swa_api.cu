@@ -1,6 +1,7 @@
 // swa_api.cu -- host side of libswa: argument checks, TMA descriptors, launch
 // configuration and the device status word.  All kernels are in the headers
 // included below, compiled into this one translation unit.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -103,10 +104,10 @@ constexpr int kMaxDevices = 64;
 
 struct DeviceInfo {
     int sms = 0;
-    bool attrs_set = false;
 };
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mu;
+thread_local int t_device = 0;                      // the current device, as device_info found it in this call
 
 swa_status_t device_info(DeviceInfo **out) {
     int dev = 0;
@@ -114,58 +115,23 @@ swa_status_t device_info(DeviceInfo **out) {
     if (dev < 0 || dev >= kMaxDevices) return SWA_ERR_UNSUPPORTED;
     std::lock_guard<std::mutex> lk(g_dev_mu);
     DeviceInfo &d = g_dev[dev];
-    if (!d.attrs_set) {
-        SWA_CUDA_TRY(cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev));
-        SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_prefill_kernel<64>,
-                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          swa::PrefillCfg<64>::SMEM_ALLOC));
-        SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_prefill_kernel<128>,
-                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          swa::PrefillCfg<128>::SMEM_ALLOC));
-        SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_keep_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          swa::kKeepMaxSmem));
-#define SWA_SET_WEIGHTS_ATTR(DD, PP)                                                          \
-    SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_prefill_weights_kernel<DD, PP>,               \
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize,           \
-                                      swa::WeightsCfg<DD, PP>::SMEM_ALLOC));
-        SWA_SET_WEIGHTS_ATTR(64, 1) SWA_SET_WEIGHTS_ATTR(64, 2) SWA_SET_WEIGHTS_ATTR(64, 3)
-        SWA_SET_WEIGHTS_ATTR(128, 1) SWA_SET_WEIGHTS_ATTR(128, 2) SWA_SET_WEIGHTS_ATTR(128, 3)
-#undef SWA_SET_WEIGHTS_ATTR
-#define SWA_SET_DECODE_ATTR(DD, GG)                                                           \
-    SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_decode_kernel<DD, GG, swa::kDecodeWindow>,    \
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize,           \
-                                      swa::DecodeCfg<DD, GG>::SMEM_BYTES));                  \
-    SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_decode_kernel<DD, GG, swa::kDecodeSinks>,     \
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize,           \
-                                      swa::DecodeCfg<DD, GG>::SMEM_BYTES));                  \
-    SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_decode_kernel<DD, GG, swa::kDecodePackedRows>, \
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize,           \
-                                      swa::DecodeCfg<DD, GG>::SMEM_BYTES));                  \
-    SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_decode_kernel<DD, GG, swa::kDecodeWindowCluster>, \
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize,           \
-                                      swa::DecodeCfg<DD, GG>::SMEM_BYTES));                  \
-    SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_decode_q8_kernel<DD, GG, swa::kDecodeWindow>, \
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize,           \
-                                      swa::DecodeQ8Cfg<DD, GG>::SMEM_BYTES));                \
-    SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_decode_q8_kernel<DD, GG, swa::kDecodeWindowCluster>, \
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize,           \
-                                      swa::DecodeQ8Cfg<DD, GG>::SMEM_BYTES));                \
-    SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_decode_scores_kernel<DD, GG, false>,          \
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize,           \
-                                      swa::DecodeScoresCfg<DD, GG>::SMEM_BYTES));            \
-    SWA_CUDA_TRY(cudaFuncSetAttribute(swa::swa_decode_scores_kernel<DD, GG, true>,           \
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize,           \
-                                      swa::DecodeScoresCfg<DD, GG>::MAX_SMEM));
-        SWA_SET_DECODE_ATTR(64, 1) SWA_SET_DECODE_ATTR(64, 2) SWA_SET_DECODE_ATTR(64, 3)
-        SWA_SET_DECODE_ATTR(64, 4) SWA_SET_DECODE_ATTR(64, 5) SWA_SET_DECODE_ATTR(64, 6)
-        SWA_SET_DECODE_ATTR(64, 7) SWA_SET_DECODE_ATTR(64, 8)
-        SWA_SET_DECODE_ATTR(128, 1) SWA_SET_DECODE_ATTR(128, 2) SWA_SET_DECODE_ATTR(128, 3)
-        SWA_SET_DECODE_ATTR(128, 4) SWA_SET_DECODE_ATTR(128, 5) SWA_SET_DECODE_ATTR(128, 6)
-        SWA_SET_DECODE_ATTR(128, 7) SWA_SET_DECODE_ATTR(128, 8)
-#undef SWA_SET_DECODE_ATTR
-        d.attrs_set = true;
-    }
+    if (d.sms == 0) SWA_CUDA_TRY(cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev));
+    t_device = dev;
     *out = &d;
+    return SWA_OK;
+}
+
+// Lets a kernel have `bytes` of dynamic shared memory (always the same for a
+// kernel; after device_info): before its first launch on each device, because setting the attribute
+// loads the kernel's code (of all kernels at the first call of the library: 3 ms).
+template <auto KERNEL>
+swa_status_t allow_smem(int bytes) {
+    static std::atomic<uint64_t> done{0};
+    static_assert(kMaxDevices <= 64, "a bit per device");
+    const uint64_t bit = uint64_t(1) << t_device;
+    if (done.load(std::memory_order_acquire) & bit) return SWA_OK;
+    SWA_CUDA_TRY(cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    done.fetch_or(bit, std::memory_order_release);
     return SWA_OK;
 }
 
@@ -186,6 +152,7 @@ swa_status_t launch_prefill(const CUtensorMap &mq, const CUtensorMap &mk, const 
                             const CUtensorMap &mkc, const CUtensorMap &mvc, const CUtensorMap &mks,
                             const CUtensorMap &mvs, const swa::PrefillParams &p, int sms, cudaStream_t s) {
     const int grid = p.num_units < sms ? p.num_units : sms;
+    if (swa_status_t e = allow_smem<swa::swa_prefill_kernel<D>>(swa::PrefillCfg<D>::SMEM_ALLOC)) return e;
     swa::swa_prefill_kernel<D><<<grid, swa::PrefillCfg<D>::THREADS, swa::PrefillCfg<D>::SMEM_ALLOC, s>>>(
         mq, mk, mv, mkc, mvc, mks, mvs, p);
     SWA_CUDA_TRY(cudaGetLastError());
@@ -264,6 +231,7 @@ swa_status_t launch_decode_cluster(const void *q, const void *kc, const void *vc
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    if (swa_status_t e = allow_smem<swa::swa_decode_kernel<D, G, MODE>>(swa::DecodeCfg<D, G>::SMEM_BYTES)) return e;
     float2 *no_ml = nullptr;
     float *no_o = nullptr;
     SWA_CUDA_TRY(cudaLaunchKernelEx(&cfg, swa::swa_decode_kernel<D, G, MODE>,
@@ -292,9 +260,13 @@ swa_status_t launch_decode_dg(const void *q, const void *kc, const void *vc, con
         return launch_decode_cluster<D, G, swa::kDecodeWindowCluster>(q, kc, vc, pos, out, B, Hkv, W, scale, rope,
                                                                       nullptr, nullptr, nullptr, B, kv_rep, s);
     dim3 grid(nsm, Hkv, B);
+    constexpr int smem = swa::DecodeCfg<D, G>::SMEM_BYTES;
     auto kernel = S > 0 ? swa::swa_decode_kernel<D, G, swa::kDecodeSinks>
                         : swa::swa_decode_kernel<D, G, swa::kDecodeWindow>;
-    kernel<<<grid, swa::kDecodeWarps * 32, swa::DecodeCfg<D, G>::SMEM_BYTES, s>>>(
+    if (swa_status_t e = S > 0 ? allow_smem<swa::swa_decode_kernel<D, G, swa::kDecodeSinks>>(smem)
+                               : allow_smem<swa::swa_decode_kernel<D, G, swa::kDecodeWindow>>(smem))
+        return e;
+    kernel<<<grid, swa::kDecodeWarps * 32, smem, s>>>(
         static_cast<const __nv_bfloat16 *>(q), static_cast<const __nv_bfloat16 *>(kc),
         static_cast<const __nv_bfloat16 *>(vc), pos, static_cast<__nv_bfloat16 *>(out), ws_ml, ws_o,
         Hkv, W, nsm, scale * kLog2e, rope ? 1 : 0, rope ? *rope : swa::RopeTable{},
@@ -757,8 +729,12 @@ swa_status_t launch_decode_q8_dg(const void *q, const void *kc, const void *vc, 
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cluster ? 1 : 0;
+    constexpr int smem = swa::DecodeQ8Cfg<D, G>::SMEM_BYTES;
     auto kernel = cluster ? swa::swa_decode_q8_kernel<D, G, swa::kDecodeWindowCluster>
                           : swa::swa_decode_q8_kernel<D, G, swa::kDecodeWindow>;
+    if (swa_status_t e = cluster ? allow_smem<swa::swa_decode_q8_kernel<D, G, swa::kDecodeWindowCluster>>(smem)
+                                 : allow_smem<swa::swa_decode_q8_kernel<D, G, swa::kDecodeWindow>>(smem))
+        return e;
     SWA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, mk, mv, static_cast<const __nv_bfloat16 *>(q), ks, vs, pos,
                                     static_cast<__nv_bfloat16 *>(out), ws_ml, ws_o, Hkv, W, nsm, scale * kLog2e,
                                     split, kv_rep, block_log2, nblk));
@@ -918,6 +894,9 @@ swa_status_t launch_decode_weights_dg(const void *q, const void *kc, const void 
         attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
+        if (swa_status_t e =
+                allow_smem<swa::swa_decode_scores_kernel<D, G, true>>(swa::DecodeScoresCfg<D, G>::MAX_SMEM))
+            return e;
         SWA_CUDA_TRY(cudaLaunchKernelEx(&cfg, swa::swa_decode_scores_kernel<D, G, true>, qb, kb, vb, slot_pos, pos,
                                         ws_ml, ws_o, scores, scores_cluster_keys(M), groups, M, 1, scale * kLog2e, 0,
                                         rep, weights, weights_out, ob));
@@ -928,6 +907,9 @@ swa_status_t launch_decode_weights_dg(const void *q, const void *kc, const void 
     ws_o = reinterpret_cast<float *>(base);
     ws_ml = reinterpret_cast<float4 *>(base + l.ml_off);
     scores = reinterpret_cast<float *>(base + l.scores_off);
+    if (swa_status_t e =
+            allow_smem<swa::swa_decode_scores_kernel<D, G, false>>(swa::DecodeScoresCfg<D, G>::SMEM_BYTES))
+        return e;
     swa::swa_decode_scores_kernel<D, G, false>
         <<<dim3(l.nsm, groups, B), swa::kDecodeWarps * 32, swa::DecodeScoresCfg<D, G>::SMEM_BYTES, s>>>(
             qb, kb, vb, slot_pos, pos, ws_ml, ws_o, scores, l.stride, groups, M, l.nsm, scale * kLog2e, l.split, rep,
@@ -995,6 +977,7 @@ swa_status_t keep_impl(const void *k, const void *v, const float *weights, const
     if (swa_status_t e = budget_checks(B, Hkv, D, M, S, R)) return e;
     DeviceInfo *dev = nullptr;
     if (swa_status_t e = device_info(&dev)) return e;
+    if (swa_status_t e = allow_smem<swa::swa_keep_select_kernel>(swa::kKeepMaxSmem)) return e;
     swa::swa_keep_select_kernel<<<dim3(Hkv, B), swa::kKeepThreads, swa::keep_smem(N), s>>>(
         weights, lens, slot_pos, weights_out, N, Hkv, M, S, R);
     SWA_CUDA_TRY(cudaGetLastError());
@@ -1065,6 +1048,8 @@ template <int D, int MODE>
 swa_status_t launch_weights_pass(const CUtensorMap &mq, const CUtensorMap &mk, const swa::WeightsParams &p, int sms,
                                  cudaStream_t s) {
     const int grid = p.num_units < sms ? p.num_units : sms;
+    if (swa_status_t e = allow_smem<swa::swa_prefill_weights_kernel<D, MODE>>(swa::WeightsCfg<D, MODE>::SMEM_ALLOC))
+        return e;
     swa::swa_prefill_weights_kernel<D, MODE>
         <<<grid, swa::WeightsCfg<D, MODE>::THREADS, swa::WeightsCfg<D, MODE>::SMEM_ALLOC, s>>>(mq, mk, p);
     SWA_CUDA_TRY(cudaGetLastError());
