@@ -330,7 +330,11 @@ swa_status_t swa_decode_rope(const void *q, const void *k_cache, const void *v_c
  * that receives a token is quantised anew from what it then holds: the new
  * tokens, and the values that its other written slots stand for.  (A scale
  * that moves rounds only elements below 2^-6 of it.)  A 16-bit rolling buffer
- * is converted by one call with pos = 0, T = W (slot s then holds slot s). */
+ * whose sequences have all reached W positions is converted by one call with pos
+ * = 0, T = W (slot s then holds slot s).  A sequence of n < W positions is
+ * converted by a call of its own with B = 1, pos = 0, T = n: all T rows count as
+ * tokens, so what the slots behind it hold would set the scale of its last block
+ * otherwise. */
 swa_status_t swa_cache_append_q8(const void *k_new, const void *v_new, void *k_cache, void *v_cache,
                                  float *k_scale, float *v_scale, const int32_t *pos, int B, int T,
                                  int Hkv, int D, int W, int block, swa_stream_t stream);
