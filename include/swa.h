@@ -481,6 +481,10 @@ swa_status_t swa_selftest_wait_timeout(swa_stream_t stream);
  */
 swa_status_t swa_selftest_exp2(const float *x, float *y, int n, swa_stream_t stream);
 
+/* swa_selftest_exp2_fine -- the same of the exponential that swa_prefill_weights
+ * uses for a share of its weights (relative error below 2.5e-7). */
+swa_status_t swa_selftest_exp2_fine(const float *x, float *y, int n, swa_stream_t stream);
+
 /* Human-readable name of a status code. */
 const char *swa_status_string(swa_status_t status);
 

@@ -21,7 +21,7 @@ __all__ = [
     "swa_decode", "swa_decode_workspace_size", "swa_decode_noalloc", "swa_prefill_varlen",
     "swa_prefill_chunk_varlen", "swa_prefill_sinks", "swa_prefill_chunk_sinks", "swa_cache_append_sinks",
     "swa_decode_sinks", "swa_rope", "swa_get_device_status", "swa_set_wait_limit_ns",
-    "swa_selftest_wait_timeout", "swa_selftest_exp2", "SWA_OK", "SWA_ERR_INVALID_ARG",
+    "swa_selftest_wait_timeout", "swa_selftest_exp2", "swa_selftest_exp2_fine", "SWA_OK", "SWA_ERR_INVALID_ARG",
     "SWA_ERR_UNSUPPORTED", "SWA_ERR_CUDA", "SWA_ERR_TIMEOUT", "SWA_WINDOW_EXCL_LEFT",
     "SWA_WINDOW_INCL_LEFT", "bounds_checked", "swa_cache_append_q8", "swa_decode_q8", "swa_prefill_chunk_q8",
     "swa_decode_q8_workspace_size",
@@ -162,8 +162,9 @@ def lib() -> ctypes.CDLL:
             L.swa_get_device_status.argtypes = [st]
             L.swa_set_wait_limit_ns.argtypes = [ctypes.c_ulonglong]
             L.swa_selftest_wait_timeout.argtypes = [st]
-            L.swa_selftest_exp2.argtypes = [vp, vp, i, st]
-            L.swa_selftest_exp2.restype = ctypes.c_int
+            for fn in (L.swa_selftest_exp2, L.swa_selftest_exp2_fine):
+                fn.argtypes = [vp, vp, i, st]
+                fn.restype = ctypes.c_int
             L.swa_status_string.argtypes = [i]
             L.swa_status_string.restype = ctypes.c_char_p
             L.swa_last_cuda_error.argtypes = []
@@ -327,15 +328,23 @@ def swa_set_wait_limit_ns(limit_ns: int) -> None:
     _check(lib().swa_set_wait_limit_ns(int(limit_ns)), "swa_set_wait_limit_ns")
 
 
-def swa_selftest_exp2(x, stream=None):
-    """2^x by the prefill kernel's FMA-pipe exponential (test hook); x float32 CUDA."""
+def _selftest_exp2(fn: str, x, stream):
     import torch
     if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dtype == torch.float32 and x.is_contiguous()):
         raise TypeError("x: expected a contiguous float32 CUDA tensor")
     y = torch.empty_like(x)
-    _check(lib().swa_selftest_exp2(x.data_ptr(), y.data_ptr(), x.numel(), _stream_handle(stream)),
-           "swa_selftest_exp2")
+    _check(getattr(lib(), fn)(x.data_ptr(), y.data_ptr(), x.numel(), _stream_handle(stream)), fn)
     return y
+
+
+def swa_selftest_exp2(x, stream=None):
+    """2^x by the prefill kernel's FMA-pipe exponential (test hook); x float32 CUDA."""
+    return _selftest_exp2("swa_selftest_exp2", x, stream)
+
+
+def swa_selftest_exp2_fine(x, stream=None):
+    """2^x by the prompt weights' FMA-pipe exponential (test hook); x float32 CUDA."""
+    return _selftest_exp2("swa_selftest_exp2_fine", x, stream)
 
 
 def swa_selftest_wait_timeout(stream=None) -> None:

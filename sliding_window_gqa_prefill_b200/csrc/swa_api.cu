@@ -366,15 +366,15 @@ swa_status_t noalloc_scratch(void **out) {
     return SWA_OK;
 }
 
+// FINE: the prompt weights' exponential, else the prefill's.
+template <bool FINE>
 __global__ void swa_selftest_exp2_kernel(const float *x, float *y, int n) {
     const int i = 2 * (blockIdx.x * blockDim.x + threadIdx.x);
-    if (i + 1 < n) {
-        const float2 r = swa::exp2_poly2(make_float2(x[i], x[i + 1]));
-        y[i] = r.x;
-        y[i + 1] = r.y;
-    } else if (i < n) {
-        y[i] = swa::exp2_poly2(make_float2(x[i], 0.f)).x;
-    }
+    if (i >= n) return;
+    const float2 v = make_float2(x[i], i + 1 < n ? x[i + 1] : 0.f);
+    const float2 r = FINE ? swa::exp2_poly2_fine(v) : swa::exp2_poly2(v);
+    y[i] = r.x;
+    if (i + 1 < n) y[i + 1] = r.y;
 }
 
 // ----------------------------------------------------------------- implementations
@@ -1380,7 +1380,15 @@ swa_status_t swa_selftest_wait_timeout(swa_stream_t stream) {
 swa_status_t swa_selftest_exp2(const float *x, float *y, int n, swa_stream_t stream) {
     if (!x || !y || n < 1) return SWA_ERR_INVALID_ARG;
     const int pairs = (n + 1) / 2;
-    swa_selftest_exp2_kernel<<<(pairs + 255) / 256, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(x, y, n);
+    swa_selftest_exp2_kernel<false><<<(pairs + 255) / 256, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(x, y, n);
+    SWA_CUDA_TRY(cudaGetLastError());
+    return SWA_OK;
+}
+
+swa_status_t swa_selftest_exp2_fine(const float *x, float *y, int n, swa_stream_t stream) {
+    if (!x || !y || n < 1) return SWA_ERR_INVALID_ARG;
+    const int pairs = (n + 1) / 2;
+    swa_selftest_exp2_kernel<true><<<(pairs + 255) / 256, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(x, y, n);
     SWA_CUDA_TRY(cudaGetLastError());
     return SWA_OK;
 }

@@ -93,9 +93,10 @@ __device__ __forceinline__ float2 lds_f32x2(uint32_t a) {
     return v;
 }
 
-// 2^x for two values on the FMA pipe, as exp2_poly2 but to the accuracy of the
-// special-function unit: degree 5, fitted in the same way (relative error
-// 1.3e-7 in fp32).  x is clamped at -126.
+// 2^x for two values on the FMA pipe, as exp2_poly2 but to about the accuracy of
+// the special-function unit: degree 5, fitted in the same way (relative error
+// 1.6e-7, with fp32 steps 2.2e-7, both at the ends of a binade).  x is clamped at
+// -126; a NaN becomes 2^-126.
 __device__ __forceinline__ float2 exp2_poly2_fine(float2 x) {
     constexpr float kShift = 12582912.0f;                       // 1.5 * 2^23
     constexpr float c1 = 0.69314694f, c2 = 0.24022120f, c3 = 0.055507131f, c4 = 0.0096755410f, c5 = 0.0013276471f;
