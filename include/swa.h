@@ -358,7 +358,10 @@ size_t swa_decode_q8_workspace_size(int B, int Hq, int Hkv, int D, int W);
  * beside those that see it, within their 128-row block, and values above 2^119
  * / W may overflow the 32-bit sums.)  workspace: at least
  * swa_prefill_chunk_q8_workspace_size() bytes, 256-byte aligned; it holds the
- * window widened to bf16 (exactly) during the call. */
+ * window widened to bf16 (exactly) during the call: 4 bytes per slot, head and
+ * element, 4 B W Hkv D, as much as a 16-bit buffer of the same size (1.07 GB at
+ * B=64, W=4096, 8 heads of 128).  One workspace serves all layers in turn; long
+ * batches can be cut into calls of fewer sequences. */
 swa_status_t swa_prefill_chunk_q8(const void *q, const void *k, const void *v, void *k_cache,
                                   void *v_cache, float *k_scale, float *v_scale,
                                   const int32_t *start_pos, void *out, int B, int C, int Hq, int Hkv,

@@ -146,7 +146,7 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t *red) {
 //
 // Bound by memory for long appends if the arithmetic per piece stays small: 4 x
 // 4000 tokens, 8 heads, D=128 (99 MB): 31 us with one path for every block and
-// scalar maxima (170 instructions a piece), 23.3 with packed maxima, 18.3 with
+// scalar maxima (170 instructions a piece), 23.3 with packed maxima, 19.2 with
 // whole blocks apart.  A step of one token for 64 sequences takes 7.5 us, mostly
 // the latency of position -> block -> scale.
 template <int BLOCK, int D>
@@ -293,8 +293,9 @@ swa_append_q8_kernel(const uint4 *__restrict__ k_new, const uint4 *__restrict__ 
 // reached, and of a full buffer the one that holds position start - W -- become
 // zeros, so that the attention's masked products there stay 0 whatever they
 // hold.  16 codes of K and of V per thread and step; grid y the sequence, x
-// strides over its vectors, slot and vector of the row carried along (a 64-bit
-// division per step made it 13.6 us at B=2, W=4096, 8 heads of 128; now 11.8).
+// strides over its vectors, slot and vector of the row carried along rather than
+// divided out of an index each step (13.6 us at B=2, W=4096, 8 heads of 128; now
+// 11.8); the scale's index still takes two divisions, by `block` and head_vec.
 __global__ void __launch_bounds__(256)
 swa_widen_q8_kernel(const uint4 *__restrict__ k_cache, const uint4 *__restrict__ v_cache,
                     const float *__restrict__ k_scale, const float *__restrict__ v_scale,

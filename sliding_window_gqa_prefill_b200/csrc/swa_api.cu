@@ -657,9 +657,20 @@ swa_status_t append_q8_impl(const void *k_new, const void *v_new, void *k_cache,
 // kQ8MergePart per split for the merge kernel.  Splits are multiples of 64 keys,
 // at least kDecodeMinSplit.  Against the 16-bit decode's rule (up to 1024 keys):
 // B=64, W=4096, 8 KV heads, one split instead of four 88 against 101 us, W=2000
-// one instead of two 49 against 58; small batches are cut alike.  A function of
-// the sizes only: the workspace size follows from it.  (The longest split keeps
-// the kernels' 32-bit sums of a window and a split in range.)
+// one instead of two 49 against 58; small batches are cut alike.  With 32 / 8
+// heads of 128 and full windows, in us: the rule's number of splits, the best of
+// 1 to 18, and one split:
+//   W=4096  B=1 10.2 (11 splits), 9.8 (18), 46    B=4 15.8 (11), 14.9 (8), 47
+//           B=8 21.1 (8), 20.0 (4), 48            B=16 30.7 (4), the best, 49
+//           B=24 41.8 (3), the best, 56           B=32 52.8 (2), the best, 57
+//           B=48 75.4 (3), 71.8 (1), 72           B=64 89 (1), the best
+//   W=1000  B=1 to 16 7.1 to 13.9 (4), the best, 14 to 16
+//           B=24 19.9 (3), 19.0 (1)               B=32 22.6 (2), 19.3 (1)
+//           B=48 24.1 (1), the best               B=64 29.5 (1), the best
+// A function of the sizes only: the workspace size follows from it, and is asked
+// for without a device, so the SM count of the B200 (148, four blocks to each) is
+// written into it; on another the results are the same.  The longest split keeps
+// the kernels' 32-bit sums of a window and a split in range.
 constexpr long long kQ8MaxSplit = 1 << 24;
 constexpr int kQ8BlocksAtOnce = 592, kQ8BlockCost = 200, kQ8MergeCost = 60, kQ8MergePart = 37;
 
@@ -846,8 +857,9 @@ bool scores_supported(int B, int Hq, int Hkv, int M) {
 
 // Slots of one block of the cluster form, and whether a call takes that form:
 // the group in one piece, at most kDecodeSplit slots to a block, and no more
-// blocks than run at once (two to an SM where their shared memory fits, 115712
-// bytes each).
+// blocks than run at once on the B200's 148 SMs (two to an SM where their shared
+// memory fits, 115712 bytes each).  As every plan behind a workspace's size it
+// depends on the sizes alone.
 int scores_cluster_keys(int M) {
     constexpr int k = swa::kDecodeClusterSplits * swa::kDecodeBlk;
     return (int)(((long long)M + k - 1) / k * swa::kDecodeBlk);
@@ -999,7 +1011,9 @@ struct WeightsLayout {
     size_t lse_off, part_off, bytes;
 };
 
-constexpr int kWeightsBlocks = 148;              // persistent blocks the splits aim at: one per SM
+// Persistent blocks the splits aim at: one per SM of the B200 (a plan behind a
+// workspace's size, so it depends on the sizes alone).
+constexpr int kWeightsBlocks = 148;
 
 // Splits of a unit's `tiles` streamed tiles.  Units of about the same work fill
 // one wave of the persistent blocks; where the work falls off along a triangle,

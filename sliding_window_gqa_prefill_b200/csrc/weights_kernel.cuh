@@ -25,17 +25,17 @@
 // loads and gives the product back halfway through, so the tensor core is up to
 // a step and a half ahead.  (One product per warpgroup, given back at three
 // quarters, is as fast; the stationary tiles as the products' operand in tensor
-// memory, three products beside them, slower: 738 against 683 us.)
+// memory, three products beside them, slower: 738 against 683 us at the time.)
 //
 // What bounds it: one exponential per score and pass, 16 per clock and SM on the
 // special-function unit: 1024 clocks for a 128 x 128 product whose MMA takes 512.
 // kWeightsPoly of 16 pairs therefore go to a polynomial on the FMA pipe (none
 // 726, 4 of 16 698, 5 720, 8 798 us).  T = N = 8192, 32 / 8 heads, D=128, both
-// passes: 683 us, 0.40 PFLOP/s of one pass's products.  At 1.55 GHz a product
+// passes: 694 us (687 to 702), 0.40 PFLOP/s of one pass's products.  At 1.55 GHz a product
 // takes 1200 clocks, in which the schedulers issue 62% of the time and no pipe is
 // above 57% busy: 6.9 instructions per score against the 4.4 of its arithmetic,
 // the rest barriers, masks and loads per 64 columns; without the exponentials it
-// still takes 880.  T = 64 of N = 16384, two sequences: 57 us.
+// still takes 880.  T = 64 of N = 16384, two sequences: 59 us.
 #pragma once
 
 #include "weights_plan.cuh"
