@@ -389,9 +389,9 @@ size_t swa_prefill_chunk_q8_workspace_size(int B, int Hkv, int D, int W);
 
 /* swa_cache_evict_append -- store the token at position pos[b], k_new, v_new
  * [B, Hkv, D], in one slot of each KV head: the slot that already holds pos[b],
- * else the lowest free one, else the lowest that holds a position behind pos[b],
- * else the one of least weight among those whose position q has S <= q <=
- * pos[b] - R (ties: the lowest slot; NaN counts as infinity).  Its slot_pos
+ * else the lowest that is free or holds a position behind pos[b], else the one of
+ * least weight among those whose position q has S <= q <= pos[b] - R (ties: the
+ * lowest slot; NaN counts as infinity).  Its slot_pos
  * becomes pos[b], its weight 0.  slots: int32 [B, Hkv], receives the slot taken,
  * or NULL.  If no slot may be evicted nothing is written, slots gets -1 and
  * SWA_ERR_INVALID_ARG is recorded (as for pos[b] < 0); it cannot happen to a

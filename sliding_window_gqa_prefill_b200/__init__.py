@@ -592,9 +592,9 @@ def swa_cache_evict_append(k_new, v_new, k_cache, v_cache, slot_pos, weights, po
                            stream=None):
     """Store the token at pos[b], k_new/v_new [B,Hkv,D] bf16, in one slot of each
     KV head of the caches [B,M,Hkv,D]: the one that holds pos[b], else the lowest
-    free one (slot_pos < 0), else the lowest that holds a position behind pos[b]
-    (of a sequence that was taken back), else the one of least weight that is
-    neither of the first S positions nor of the last R.  Updates slot_pos int32 and weights
+    that is free (slot_pos < 0) or holds a position behind pos[b] (of a sequence
+    that was taken back), else the one of least weight that is neither of the
+    first S positions nor of the last R.  Updates slot_pos int32 and weights
     float32 [B,Hkv,M]; returns the slots taken, int32 [B,Hkv] (-1: none)."""
     import torch
     dev = torch.cuda.current_device()

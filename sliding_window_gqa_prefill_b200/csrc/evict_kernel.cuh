@@ -445,12 +445,14 @@ __device__ __forceinline__ uint32_t weight_order(float w) {
 }
 
 // One new token per sequence at position p = pos[b]; in each KV head it takes
-// the slot that already holds p, else the first free slot, else the first that
-// holds a position behind p (of a sequence that was taken back; the decode does
-// not see it), else the slot of least weight among those whose position q is
-// neither a sink nor recent (S <= q <= p - R; ties: the lowest slot).  One block
-// per (sequence, KV head): the choice is the minimum over the slots of one 64-bit
-// number, {kind, order of the weight, slot}, so it does not depend on the schedule.  8 bytes
+// the slot that already holds p, else the first that is free or holds a position
+// behind p (of a sequence that was taken back; the decode does not see it), else
+// the slot of least weight among those whose position q is neither a sink nor
+// recent (S <= q <= p - R; ties: the lowest slot).  The slots before the first of
+// the second kind hold different positions below p, so its index is at most p and
+// the decode, which looks at slots 0 .. p, finds it.  One block per (sequence, KV
+// head): the choice is the minimum over the slots of one 64-bit number, {kind,
+// order of the weight, slot}, so it does not depend on the schedule.  8 bytes
 // are read per slot; the kernel is bound by that and, for small batches, by
 // the latency of one pass.
 constexpr int kEvictThreads = 256;
@@ -499,9 +501,8 @@ swa_evict_append_kernel(const uint4 *__restrict__ k_new, const uint4 *__restrict
             const int s = s0 + (i / V * kEvictThreads + threadIdx.x) * V + i % V;
             unsigned long long key = ~0ull;
             if (at[i] >= S && at[i] <= last)
-                key = (3ull << 62) | ((unsigned long long)weight_order(w[i]) << 30) | (unsigned)s;
-            if (at[i] > p) key = (2ull << 62) | (unsigned)s;
-            if (at[i] < 0) key = (1ull << 62) | (unsigned)s;
+                key = (2ull << 62) | ((unsigned long long)weight_order(w[i]) << 30) | (unsigned)s;
+            if ((unsigned)at[i] > (unsigned)p) key = (1ull << 62) | (unsigned)s;      // free, or behind p
             if (at[i] == p) key = (unsigned)s;
             if (s < M) best = key < best ? key : best;
         }

@@ -69,9 +69,9 @@ def test_positions_behind_the_sequence_are_not_seen(B, Hq, H, D, M):
 
 
 def evict(held, w, p, S, R):
-    """The slot that position p takes: its own, else the lowest free one, else the
-    lowest that holds a position behind p, else the one of least weight."""
-    for want in (lambda x: x == p, lambda x: x < 0, lambda x: x > p):
+    """The slot that position p takes: its own, else the lowest that is free or
+    holds a position behind p, else the one of least weight."""
+    for want in (lambda x: x == p, lambda x: x < 0 or x > p):
         for s, x in enumerate(held):
             if want(x):
                 return s
@@ -100,9 +100,28 @@ def test_a_run_that_is_taken_back_and_goes_on(M, S, R, back):
 
 def test_order_of_the_choices():
     rng = np.random.default_rng(3)
-    at = np.array([[[11, 3, -1, 10], [11, 3, 12, 10], [12, 11, 3, 4], [3, 12, 4, 13]]])
-    w = np.array([[[0, 0, 9, 9], [0, 0, 0, 9], [9, 9, 0, 0], [0, 9, 0, 5]]], np.float32)
-    k, c = rows(rng, 1, 4, 64), rows(rng, 1, 4, 4, 64)
+    at = np.array([[[11, 3, -1, 10], [11, 3, 12, 10], [12, 11, 3, 4], [3, 12, 4, 13], [3, 12, -1, 4], [3, -1, 12, 4]]])
+    w = np.array([[[0, 0, 9, 9], [0, 0, 0, 9], [9, 9, 0, 0], [0, 9, 0, 5], [0, 9, 9, 0], [0, 9, 9, 0]]], np.float32)
+    k, c = rows(rng, 1, 6, 64), rows(rng, 1, 4, 6, 64)
     got = swa.swa_cache_evict_append(k, k, c, c.clone(), i32(at), torch.tensor(w, device="cuda"), i32([10]), 0, 2)
-    # its own slot, its own slot, the lowest behind it, the lowest behind it (weights do not matter)
-    assert got.tolist() == [[3, 3, 0, 1]]
+    # its own slot twice, then the lowest that is free or behind it (weights do not matter)
+    assert got.tolist() == [[3, 3, 0, 1, 1, 1]]
+
+
+def test_a_token_is_found_by_the_decode_that_follows_it():
+    """A long full cache, one slot of which the caller freed, taken back to a
+    position below the free slot's index: the token and its position's share of
+    the weight are seen."""
+    rng = np.random.default_rng(5)
+    M, p = 256, 50
+    held = np.arange(M)
+    held[[20, 50]] = [700, 800]
+    held[200] = -1
+    kc, vc = rows(rng, 1, M, 1, 64), rows(rng, 1, M, 1, 64)
+    at, w = i32(held[None, None]), torch.zeros(1, 1, M, device="cuda")
+    k, v, q = rows(rng, 1, 1, 64), rows(rng, 1, 1, 64), rows(rng, 1, 2, 64)
+    assert swa.swa_cache_evict_append(k, v, kc, vc, at, w, i32([p]), 4, 16).tolist() == [[20]]
+    w0 = w.clone()
+    out, _ = swa.swa_decode_weights(q, kc, vc, at, w, i32([p]), 0.125)
+    check_decode(q, kc, vc, at, w0, w, out, [p], 0.125)
+    assert w[0, 0, 20] > 0
