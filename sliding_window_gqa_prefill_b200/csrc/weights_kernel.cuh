@@ -33,7 +33,7 @@
 // 726, 4 of 16 698, 5 720, 8 798 us).  T = N = 8192, 32 / 8 heads, D=128, both
 // passes: 694 us (687 to 702), 0.40 PFLOP/s of one pass's products.  At 1.55 GHz a product
 // takes 1200 clocks, in which the schedulers issue 62% of the time and no pipe is
-// above 57% busy: 6.9 instructions per score against the 4.4 of its arithmetic,
+// above 62% busy: 6.9 instructions per score against the 4.4 of its arithmetic,
 // the rest barriers, masks and loads per 64 columns; without the exponentials it
 // still takes 880.  T = 64 of N = 16384, two sequences: 59 us.
 #pragma once
